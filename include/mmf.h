@@ -272,6 +272,101 @@ mmf_status mmf_bitlinear_backward(const void* x, mmf_dtype xdt, int64_t T, int64
                                   float* dW, float* dnorm_w, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* ---- 8-bit projection -----------------------------------------------------------------------
+ * For layers that are not ternarised (an output head, odd layers): weights as int8 codes with one
+ * scale for each output channel, times the activation codes of mmf_quantize_activations.  The
+ * pages name low-precision integer products only in general ([P5], aidev.bluegarage.site,
+ * "量子化"); the library computes, for W [N x K]:
+ *   s_n  = max_k |W_nk| / 127
+ *   c_nk = clamp(round_half_even(W_nk / s_n), -127, 127)   (divisions in float; s_n = 0: code 0)
+ *   y_tn = (sum_k q_tk c_nk) * (gamma_t / 127 * s_n)       (sum exact in int32, then float)
+ * Shapes: 1 <= T <= 16777216; N % 8 == 0, 8 <= N <= 2^20; K % 16 == 0, 16 <= K <= 32768 (for
+ * mmf_int8_forward, whose pre-pass takes the forward's K: K % 128 == 0, K <= 8192).  All matrices
+ * row-major and contiguous, 16-byte aligned, W finite.  Errors as for the forward.  Asynchronous
+ * on `stream`. */
+mmf_status mmf_int8_quantize_weights(const void* W, mmf_dtype wdt, int64_t N, int64_t K,
+                                     int8_t* W8, float* wscale, void* stream);
+
+/* y [T x N] (ydt: f32 or f16) from codes A [T x K] (any int8 values) with scales gamma [T].
+ * Needs no workspace; one launch. */
+mmf_status mmf_int8_forward_quantized(const int8_t* A, const float* gamma, int64_t T, int64_t K,
+                                      const int8_t* W8, const float* wscale, int64_t N, void* y,
+                                      mmf_dtype ydt, void* stream);
+
+/* Bytes of workspace of mmf_int8_forward: the codes [T x K] and gamma [T], each rounded up to 256
+ * bytes.  0 for unsupported T or K. */
+size_t mmf_int8_workspace_bytes(int64_t T, int64_t K);
+
+/* RMSNorm + activation quantisation of x [T x K] (as mmf_bitlinear_forward), then the product. */
+mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
+                            const float* norm_w, float eps, const int8_t* W8,
+                            const float* wscale, int64_t N, void* y, mmf_dtype ydt, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ---- linear attention with a decay for each head --------------------------------------------
+ * A token mixer beside the MLGRU: the state of a head is a matrix S [dk x dv], and a token decays
+ * it, adds an outer product and reads it with its query ([P4] "Kernkomponenten: MLGRU und GLU"
+ * has the element-wise recurrence; the pages do not name this one):
+ *   S_t = gamma_h S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   gamma_h = exp(log_decay_h)
+ * log_decay: [H] floats on the device, at most 0; values above 0 and NaN count as 0 (no decay),
+ * -inf is a decay of 0 (a token sees itself alone).  States are fp32 [B x H x dk x dv], sums and
+ * states are held in fp32.
+ *
+ * q, k [T x H x dk], v, o [T x H x dv], all of dtype dt, the last dimension contiguous; *_t and
+ * *_h are the strides of a token and of a head in elements, multiples of 16 bytes, not negative
+ * (0 shares a row between heads or tokens; not for o).  Tokens are packed: with cu_seqlens
+ * ([B + 1] int32 on the device, ascending, within 0..T) sequence b has the tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
+ * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are neither read nor
+ * written.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is
+ * touched, the outputs are then unspecified and mmf_get_device_status returns MMF_ERR_PLAN.
+ * Shapes: 1 <= T <= 16777216, 1 <= B <= 2^20, 1 <= H <= 4096, dk and dv multiples of 8 from 8 to
+ * 256.  Pointers to matrices are 16-byte aligned, ws is 256-byte aligned (NULL with ws_bytes 0
+ * when the query gives 0).  The workspace holds nothing between calls; calls that may overlap
+ * need one each.  Errors as for the forward.  Asynchronous on `stream`; may be captured into a
+ * CUDA graph. */
+typedef struct {
+  int64_t T;                    /* tokens of all sequences */
+  int64_t B;                    /* sequences */
+  const int32_t* cu_seqlens;    /* device, or NULL */
+  int32_t H, dk, dv;
+  mmf_dtype dt;                 /* of q, k, v, o and of dq, dk, dv */
+  float scale;
+  const float* log_decay;       /* device, [H] */
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+} mmf_linattn_desc;
+
+/* Workspace bytes of the forward and of the backward (0 where none is needed, and for a
+ * descriptor outside the limits). */
+size_t mmf_linattn_workspace_bytes(const mmf_linattn_desc* d);
+size_t mmf_linattn_backward_workspace_bytes(const mmf_linattn_desc* d);
+
+/* Whole prompts.  h0: states before the first tokens, or NULL (zero); hT: receives the states
+ * after the last, or NULL; hT may be h0.  A sequence without tokens has hT = h0. */
+mmf_status mmf_linattn_forward(const mmf_linattn_desc* d, const void* q, const void* k,
+                               const void* v, const float* h0, void* o, float* hT, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Gradients, from dout (dtype and strides of o) and dhT (the gradient of hT, or NULL):
+ *   R_t = U + scale q_t dout_t^T,  U = gamma R_t, last token first, U = dhT at the start
+ *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dh0 = U at the end
+ * h0: as for the forward.  dq, dk [T x H x dk] and dv [T x H x dv] are contiguous, one row for
+ * each head (of a row shared by heads the caller adds them up); dh0 (or NULL) fp32, not dhT
+ * itself.  log_decay is a constant: it gets no gradient. */
+mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void* q, const void* k,
+                                const void* v, const void* dout, const float* h0,
+                                const float* dhT, void* dq, void* dk, void* dv, float* dh0,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* One token of each of B sequences (T == B, cu_seqlens NULL): state is updated in place.  slots
+ * NULL with n_slots 0: row b has state b.  Otherwise state has n_slots states and slots[b]
+ * (device) names row b's; a negative slot is padding: o is zeros and no state is touched.  The
+ * same goes for a slot from n_slots on and for one that an earlier row has named already;
+ * mmf_get_device_status then returns MMF_ERR_PLAN. */
+mmf_status mmf_linattn_step(const mmf_linattn_desc* d, const void* q, const void* k,
+                            const void* v, void* o, float* state, const int32_t* slots,
+                            int64_t n_slots, void* stream);
+
 /* ---- forward without any allocation ------------------------------------------------------ */
 
 /* The pages have no counterpart to this entry point; it serves callers that cannot call

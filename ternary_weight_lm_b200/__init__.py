@@ -7,8 +7,10 @@ is missing, calls raise.
 
 The functions named ``mmf_*`` mirror the C ABI in ``include/mmf.h`` one to one and take
 tensors that the caller owns.  ``quantize_weights``, ``bitlinear_forward``,
-``bitlinear_glu_forward``, ``mlgru_forward`` and ``bitlinear_backward`` are conveniences that
-allocate the outputs and the workspace with torch and then call the same entry points.
+``bitlinear_glu_forward``, ``mlgru_forward``, ``bitlinear_backward``, ``quantize_weights_int8``,
+``int8_matmul``, ``int8_linear_forward``, ``linattn_forward``, ``linattn_step`` and
+``linattn_backward`` are conveniences that allocate the outputs and the workspace with torch and
+then call the same entry points.
 """
 import ctypes
 import os
@@ -25,7 +27,11 @@ __all__ = [
     "Program", "quantize_weights", "bitlinear_forward", "bitlinear_glu_forward", "workspace",
     "mmf_mlgru_workspace_bytes", "mmf_mlgru_forward", "mmf_mlgru_forward_quantized",
     "mlgru_forward", "mmf_backward_workspace_bytes", "mmf_bitlinear_backward",
-    "bitlinear_backward",
+    "bitlinear_backward", "mmf_int8_quantize_weights", "mmf_int8_forward_quantized",
+    "mmf_int8_workspace_bytes", "mmf_int8_forward", "quantize_weights_int8", "int8_matmul",
+    "int8_linear_forward", "LinattnDesc", "mmf_linattn_workspace_bytes",
+    "mmf_linattn_backward_workspace_bytes", "mmf_linattn_forward", "mmf_linattn_backward",
+    "mmf_linattn_step", "linattn_forward", "linattn_step", "linattn_backward",
     "MMF_F32", "MMF_F16", "STATUS",
 ]
 
@@ -53,6 +59,16 @@ class Projection(ctypes.Structure):
                 ("Wp", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("K", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("glu", ctypes.c_int32), ("level", ctypes.c_int32),
                 ("y", ctypes.c_void_p), ("ydt", ctypes.c_int)]
+
+
+class LinattnDesc(ctypes.Structure):
+    """Mirror of the C struct mmf_linattn_desc (sizes and strides of a linear attention call)."""
+    _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+                ("H", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dt", ctypes.c_int), ("scale", ctypes.c_float), ("log_decay", ctypes.c_void_p),
+                ("q_t", ctypes.c_int64), ("q_h", ctypes.c_int64), ("k_t", ctypes.c_int64),
+                ("k_h", ctypes.c_int64), ("v_t", ctypes.c_int64), ("v_h", ctypes.c_int64),
+                ("o_t", ctypes.c_int64), ("o_h", ctypes.c_int64)]
 
 
 _lib = None
@@ -87,6 +103,15 @@ def lib():
             "mmf_mlgru_forward": ([P, P, P, I, I64, I64, P, P, F, P, I, P, P, SZ, P], I),
             "mmf_mlgru_forward_quantized": ([P, P, P, I, I64, I64, P, P, F, P, F, P, P, P, P, P,
                                              SZ, P], I),
+            "mmf_int8_quantize_weights": ([P, I, I64, I64, P, P, P], I),
+            "mmf_int8_forward_quantized": ([P, P, I64, I64, P, P, I64, P, I, P], I),
+            "mmf_int8_workspace_bytes": ([I64, I64], SZ),
+            "mmf_int8_forward": ([P, I, I64, I64, P, F, P, P, I64, P, I, P, SZ, P], I),
+            "mmf_linattn_workspace_bytes": ([P], SZ),
+            "mmf_linattn_backward_workspace_bytes": ([P], SZ),
+            "mmf_linattn_forward": ([P, P, P, P, P, P, P, P, SZ, P], I),
+            "mmf_linattn_backward": ([P, P, P, P, P, P, P, P, P, P, P, P, SZ, P], I),
+            "mmf_linattn_step": ([P, P, P, P, P, P, P, I64, P], I),
             "mmf_program_workspace_bytes": ([P, I, I64], SZ),
             "mmf_program_init": ([P, I, I64, F, P, SZ, P], I),
             "mmf_program_run": ([P, P], I),
@@ -253,6 +278,64 @@ def mmf_mlgru_forward_quantized(I, F, G, h0, norm_w, eps, oproj_norm_w, oproj_ep
         wn, _stream(stream)))
 
 
+def mmf_int8_quantize_weights(W, W8, wscale, stream=None):
+    """W [N, K] -> int8 codes W8 [N, K] and one scale for each row (include/mmf.h)."""
+    N, K = W.shape
+    _check("mmf_int8_quantize_weights", lib().mmf_int8_quantize_weights(
+        _ptr(W), _dt(W), N, K, _ptr(W8), _ptr(wscale), _stream(stream)))
+
+
+def mmf_int8_forward_quantized(A, gamma, W8, wscale, y, stream=None):
+    """y [T, N] from activation codes A [T, K], gamma [T] and 8-bit weights."""
+    T, K = A.shape
+    _check("mmf_int8_forward_quantized", lib().mmf_int8_forward_quantized(
+        _ptr(A), _ptr(gamma), T, K, _ptr(W8), _ptr(wscale), W8.shape[0], _ptr(y), _dt(y),
+        _stream(stream)))
+
+
+def mmf_int8_workspace_bytes(T, K):
+    return lib().mmf_int8_workspace_bytes(T, K)
+
+
+def mmf_int8_forward(x, norm_w, eps, W8, wscale, y, ws, stream=None):
+    T, K = x.shape
+    _check("mmf_int8_forward", lib().mmf_int8_forward(
+        _ptr(x), _dt(x), T, K, _ptr(norm_w), float(eps), _ptr(W8), _ptr(wscale), W8.shape[0],
+        _ptr(y), _dt(y), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def mmf_linattn_workspace_bytes(desc):
+    return lib().mmf_linattn_workspace_bytes(ctypes.byref(desc))
+
+
+def mmf_linattn_backward_workspace_bytes(desc):
+    return lib().mmf_linattn_backward_workspace_bytes(ctypes.byref(desc))
+
+
+def mmf_linattn_forward(desc, q, k, v, h0, o, hT=None, ws=None, stream=None):
+    """Linear attention over whole prompts (include/mmf.h); desc: a LinattnDesc."""
+    wp, wn = _ws(ws)
+    _check("mmf_linattn_forward", lib().mmf_linattn_forward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(h0), _ptr(o), _ptr(hT), wp, wn,
+        _stream(stream)))
+
+
+def mmf_linattn_backward(desc, q, k, v, dout, h0, dhT, dq, dk, dv, dh0=None, ws=None,
+                         stream=None):
+    wp, wn = _ws(ws)
+    _check("mmf_linattn_backward", lib().mmf_linattn_backward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(h0), _ptr(dhT), _ptr(dq),
+        _ptr(dk), _ptr(dv), _ptr(dh0), wp, wn, _stream(stream)))
+
+
+def mmf_linattn_step(desc, q, k, v, o, state, slots=None, stream=None):
+    """One token of each sequence; state is updated in place."""
+    n = 0 if slots is None else state.shape[0]
+    _check("mmf_linattn_step", lib().mmf_linattn_step(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(state), _ptr(slots), n,
+        _stream(stream)))
+
+
 def _proj_array(projs):
     arr = (Projection * len(projs))()
     for i, p in enumerate(projs):
@@ -385,3 +468,189 @@ def bitlinear_backward(x, Wp, beta, dy, norm_w=None, eps=1e-8, A=None, gamma=Non
         ws = workspace(mmf_backward_workspace_bytes(T, K, N), dev)
     mmf_bitlinear_backward(x, norm_w, eps, A, gamma, Wp, beta, N, dy, dx, dW, dg, ws, stream)
     return dx, dW, dg
+
+
+# ------------------------------------------------------------- 8-bit projection, linear attention
+def _tensor(name, t, shape, dtypes, device, contiguous=True):
+    """Refuses a tensor that the call would misread."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not contiguous and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+class _On:
+    """Makes a tensor's device and the call's stream current, so that what the call allocates
+    belongs to the stream that uses it; ``handle`` is the stream's."""
+
+    def __init__(self, t, stream):
+        import torch
+        if t.device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, got {t.device}")
+        self.device = torch.cuda.device(t.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        self.given = stream
+
+    def __enter__(self):
+        import torch
+        self.device.__enter__()
+        s = torch.cuda.current_stream() if self.given is None else self.given
+        self.stream = torch.cuda.stream(s)
+        self.stream.__enter__()
+        self.handle = s.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def quantize_weights_int8(W, stream=None):
+    """W [N, K] (fp32/fp16, CUDA, contiguous) -> (W8 int8 [N, K], wscale float32 [N])."""
+    import torch
+    _tensor("W", W, (None, None), (torch.float32, torch.float16), W.device)
+    with _On(W, stream) as on:
+        W8 = torch.empty(W.shape, dtype=torch.int8, device=W.device)
+        wscale = torch.empty(W.shape[0], dtype=torch.float32, device=W.device)
+        mmf_int8_quantize_weights(W, W8, wscale, on.handle)
+    return W8, wscale
+
+
+def int8_matmul(A, gamma, W8, wscale, out_dtype=None, out=None, stream=None):
+    """y [T, N] of activation codes A [T, K] with scales gamma [T] (mmf_quantize_activations) and
+    weights from quantize_weights_int8; fp16 unless out_dtype or out says otherwise."""
+    import torch
+    _tensor("A", A, (None, None), torch.int8, A.device)
+    T, K = A.shape
+    _tensor("W8", W8, (None, K), torch.int8, A.device)
+    N = W8.shape[0]
+    _tensor("gamma", gamma, (T,), torch.float32, A.device)
+    _tensor("wscale", wscale, (N,), torch.float32, A.device)
+    if out is not None:
+        _tensor("out", out, (T, N), (torch.float32, torch.float16), A.device)
+    with _On(A, stream) as on:
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype or torch.float16, device=A.device)
+        mmf_int8_forward_quantized(A, gamma, W8, wscale, out, on.handle)
+    return out
+
+
+def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws=None,
+                        stream=None):
+    """RMSNorm, activation quantisation and 8-bit product of x [T, K]: y [T, N]."""
+    import torch
+    f = (torch.float32, torch.float16)
+    _tensor("x", x, (None, None), f, x.device)
+    T, K = x.shape
+    _tensor("W8", W8, (None, K), torch.int8, x.device)
+    N = W8.shape[0]
+    _tensor("wscale", wscale, (N,), torch.float32, x.device)
+    if norm_w is not None:
+        _tensor("norm_w", norm_w, (K,), torch.float32, x.device)
+    with _On(x, stream) as on:
+        y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+        if ws is None:
+            ws = workspace(mmf_int8_workspace_bytes(T, K), x.device)
+        mmf_int8_forward(x, norm_w, eps, W8, wscale, y, ws, on.handle)
+    return y
+
+
+def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
+    """Checks a call's tensors and describes them."""
+    import torch
+    dev, f = q.device, (torch.float32, torch.float16)
+    _tensor("q", q, (None, None, None), f, dev, contiguous=False)
+    T, H, dk = q.shape
+    _tensor("k", k, (T, H, dk), q.dtype, dev, contiguous=False)
+    _tensor("v", v, (T, H, None), q.dtype, dev, contiguous=False)
+    dv = v.shape[2]
+    _tensor("log_decay", log_decay, (H,), torch.float32, dev)
+    if o is not None:
+        _tensor("out", o, (T, H, dv), q.dtype, dev, contiguous=False)
+    if cu_seqlens is not None:
+        _tensor("cu_seqlens", cu_seqlens, (None,), torch.int32, dev)
+        if batch is not None and batch != cu_seqlens.numel() - 1:
+            raise ValueError(f"batch {batch}, but cu_seqlens has {cu_seqlens.numel() - 1} sequences")
+        batch = cu_seqlens.numel() - 1
+    d = LinattnDesc()
+    d.T, d.B, d.H, d.dk, d.dv = T, 1 if batch is None else batch, H, dk, dv
+    d.cu_seqlens, d.dt, d.log_decay = _ptr(cu_seqlens), _dt(q), _ptr(log_decay)
+    d.scale = dk ** -0.5 if scale is None else scale
+    d.q_t, d.q_h, d.k_t, d.k_h = q.stride(0), q.stride(1), k.stride(0), k.stride(1)
+    d.v_t, d.v_h = v.stride(0), v.stride(1)
+    d.o_t, d.o_h = (H * dv, dv) if o is None else (o.stride(0), o.stride(1))
+    return d
+
+
+def _linattn_ws(ws, need, device):
+    return ws if ws is not None or need == 0 else workspace(need, device)
+
+
+def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None, h0=None, hT=None,
+                    out=None, ws=None, stream=None):
+    """Linear attention with a decay for each head over packed prompts: o [T, H, dv].
+
+    q, k [T, H, dk], v [T, H, dv] of one dtype (fp16 or fp32), views with any token and head
+    strides of whole 16 bytes; log_decay [H] fp32, at most 0; scale: dk ** -0.5 unless given.
+    cu_seqlens [B + 1] int32 (device), or batch equal sequences (1 unless given).  h0, hT
+    [B, H, dk, dv] fp32: states before (zero unless given) and after (written if given; may be
+    h0)."""
+    import torch
+    d = _linattn(q, k, v, log_decay, out, scale, cu_seqlens, batch)
+    state = (d.B, d.H, d.dk, d.dv)
+    for name, t in (("h0", h0), ("hT", hT)):
+        if t is not None:
+            _tensor(name, t, state, torch.float32, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
+        ws = _linattn_ws(ws, mmf_linattn_workspace_bytes(d), q.device)
+        mmf_linattn_forward(d, q, k, v, h0, out, hT, ws, on.handle)
+    return out
+
+
+def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, stream=None):
+    """One new token of each of B sequences: o [B, H, dv]; q, k [B, H, dk], v [B, H, dv].
+
+    state [B, H, dk, dv] fp32 is updated in place; with slots [B] int32 (device) it is a pool
+    [n, H, dk, dv] and slots names each row's state (negative: padding, zeros out)."""
+    import torch
+    d = _linattn(q, k, v, log_decay, out, scale, None, q.shape[0])
+    _tensor("state", state, (None if slots is not None else d.B, d.H, d.dk, d.dv), torch.float32,
+            q.device)
+    if slots is not None:
+        _tensor("slots", slots, (d.B,), torch.int32, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = torch.empty((d.B, d.H, d.dv), dtype=q.dtype, device=q.device)
+        mmf_linattn_step(d, q, k, v, out, state, slots, on.handle)
+    return out
+
+
+def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batch=None, h0=None,
+                     dhT=None, want_dh0=False, ws=None, stream=None):
+    """Gradients of linattn_forward: ``(dq, dk, dv, dh0)`` (dh0 None unless asked for).
+
+    dout [T, H, dv]: the gradient of o; dhT: that of hT (none unless given).  Rows of tokens
+    outside the sequences are not written."""
+    import torch
+    d = _linattn(q, k, v, log_decay, dout, scale, cu_seqlens, batch)
+    state = (d.B, d.H, d.dk, d.dv)
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None:
+            _tensor(name, t, state, torch.float32, q.device)
+    with _On(q, stream) as on:
+        dq, dk = (torch.empty((d.T, d.H, d.dk), dtype=q.dtype, device=q.device) for _ in range(2))
+        dv = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
+        dh0 = torch.empty(state, dtype=torch.float32, device=q.device) if want_dh0 else None
+        ws = _linattn_ws(ws, mmf_linattn_backward_workspace_bytes(d), q.device)
+        mmf_linattn_backward(d, q, k, v, dout, h0, dhT, dq, dk, dv, dh0, ws, on.handle)
+    return dq, dk, dv, dh0

@@ -1,0 +1,387 @@
+// Linear attention with a decay for each head: S_t = gamma S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+//
+// A token mixer of the family of the MLGRU (an element-wise recurrence, "MatMul-freie LLMs:
+// Zentrale Konzepte erklärt", section "Kernkomponenten: MLGRU und GLU"), with a matrix for a
+// state.  This file holds the token-by-token sweep for every type and head size, the pass that
+// joins the segments of a split sequence, and the single-token step.
+//
+// Splitting.  A sweep is serial in the tokens, so when (sequence, head) pairs are too few to fill
+// the GPU every sequence is cut into segments of L tokens: one pass finds each segment's own
+// contribution to the state from k and v alone (kState), a second joins them,
+//   start_{s+1} = gamma^L start_s + own_s,
+// and the third runs all segments at once from their start states.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "linattn.cuh"
+#include "linattn_dev.cuh"
+#include "ptx.cuh"
+
+namespace mmf {
+namespace {
+
+// ------------------------------------------------------------------ token-by-token sweep
+// Block: one segment, one head, 32 columns of the state.  Thread (r, c) holds rows 4 r + 64 j ..
+// + 3 and columns 4 c .. + 3: 4 KR values in registers, in fp32 throughout (the products too).
+// Per token and state element: decay, update, product with q, three operations of the fp32 pipe,
+// which is what bounds it (148 SMs x 128 lanes); k, q and v come from shared memory as 16-byte
+// broadcasts.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
+// through shared memory once every kTok tokens.
+constexpr int kSweepThreads = 128;
+constexpr int kTok = 16;
+constexpr int kCols = 32;
+
+template <typename T>
+__device__ __forceinline__ float4 ld4(const T* p);
+template <>
+__device__ __forceinline__ float4 ld4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 ld4<__half>(const __half* p) {
+  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&a.x));
+  const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&a.y));
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
+__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st1(__half* p, float v) { *p = __float2half_rn(v); }
+
+template <typename T, int KR, bool kState>
+__global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_constant__ LinCall c) {
+  constexpr int kRows = 16 * KR;           // padded dk
+  constexpr int kVecRow = kRows / 4;       // 4-value vectors of a k or q row
+  constexpr int kLoads = kTok * kVecRow / kSweepThreads;   // of k (and of q) per thread
+  static_assert(kTok * (kCols / 4) == kSweepThreads, "one v vector per thread");
+  __shared__ __align__(16) float s_k[kTok][kRows];
+  __shared__ __align__(16) float s_q[kState ? 1 : kTok][kState ? 4 : kRows];
+  __shared__ __align__(16) float s_v[kTok][kCols];
+  __shared__ float s_o[kState ? 1 : 4][kState ? 1 : kTok][kCols];
+
+  const int slices = (max(c.sw[0].dv, c.sw[0].dk) + kCols - 1) / kCols;
+  const LinSweep& w = c.sw[blockIdx.z / slices];
+  const int col0 = static_cast<int>(blockIdx.z % slices) * kCols;
+  if (col0 >= w.dv) return;
+  const int h = blockIdx.y;
+  const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
+  if (!g.valid || (kState && (g.last || g.n == 0))) return;
+
+  const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3, warp = tid >> 5;
+  LinGamma gamma(lin_lg2(c, h));
+  const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
+  float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
+
+  // the state before the first token: the split's start state [dk x dv], or s0
+  float S[KR][4];
+#pragma unroll
+  for (int i = 0; i < KR; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 4 * rg + (i & 3) + 64 * (i >> 2), col = col0 + 4 * cg + j;
+      float x = 0.0f;
+      if (!kState && row < w.dk && col < w.dv) {
+        if (c.split && !(g.first && g.last))   // one segment: nothing was joined
+          x = seg[static_cast<size_t>(row) * w.dv + col];
+        else if (w.s0)
+          x = w.s0[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val];
+      }
+      S[i][j] = x;
+    }
+
+  const T* kp = static_cast<const T*>(w.k) + h * w.k_h;
+  const T* vp = static_cast<const T*>(w.v) + h * w.v_h;
+  const T* qp = static_cast<const T*>(w.q) + h * w.q_h;
+  T* op = static_cast<T*>(w.o) + h * w.o_h;
+  const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 rk[kLoads], rq[kState ? 1 : kLoads], rv;
+
+  auto fetch = [&](int64_t p0) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int x = tid + i * kSweepThreads, tok = x / kVecRow, d = (x % kVecRow) * 4;
+      const bool in = p0 + tok < g.n && d < w.dk;
+      const int64_t t = g.token(p0 + tok);
+      rk[i] = in ? ld4<T>(kp + t * w.k_t + d) : zero4;
+      if constexpr (!kState) rq[i] = in ? ld4<T>(qp + t * w.q_t + d) : zero4;
+    }
+    const int tok = tid / (kCols / 4), d = col0 + (tid % (kCols / 4)) * 4;
+    rv = (p0 + tok < g.n && d < w.dv) ? ld4<T>(vp + g.token(p0 + tok) * w.v_t + d) : zero4;
+  };
+
+  // forwards the decay acts before a token is added, backwards after it: held back until the next
+  float dec = w.backwards ? 1.0f : gamma.next();
+  fetch(0);
+  for (int64_t p0 = 0; p0 < g.n; p0 += kTok) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int x = tid + i * kSweepThreads, tok = x / kVecRow, d = (x % kVecRow) * 4;
+      *reinterpret_cast<float4*>(&s_k[tok][d]) = rk[i];
+      if constexpr (!kState) *reinterpret_cast<float4*>(&s_q[tok][d]) = rq[i];
+    }
+    *reinterpret_cast<float4*>(&s_v[tid / (kCols / 4)][(tid % (kCols / 4)) * 4]) =
+        make_float4(rv.x * w.a, rv.y * w.a, rv.z * w.a, rv.w * w.a);
+    __syncthreads();
+    if (p0 + kTok < g.n) fetch(p0 + kTok);
+    const int nt = static_cast<int>(min(static_cast<int64_t>(kTok), g.n - p0));
+    for (int tok = 0; tok < nt; ++tok) {
+      const float4 v4 = *reinterpret_cast<const float4*>(&s_v[tok][4 * cg]);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i4 = 0; i4 < KR / 4; ++i4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&s_k[tok][4 * rg + 64 * i4]);
+        const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+        float qq[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!kState) {
+          const float4 q4 = *reinterpret_cast<const float4*>(&s_q[tok][4 * rg + 64 * i4]);
+          qq[0] = q4.x; qq[1] = q4.y; qq[2] = q4.z; qq[3] = q4.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* Sr = S[4 * i4 + i];
+          Sr[0] = fmaf(kk[i], v4.x, dec * Sr[0]);
+          Sr[1] = fmaf(kk[i], v4.y, dec * Sr[1]);
+          Sr[2] = fmaf(kk[i], v4.z, dec * Sr[2]);
+          Sr[3] = fmaf(kk[i], v4.w, dec * Sr[3]);
+          if constexpr (!kState) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = fmaf(qq[i], Sr[j], acc[j]);
+          }
+        }
+      }
+      dec = gamma.next();
+      if constexpr (!kState) {
+        // sum over the warp's four row groups (lane bits 3 and 4); each lane ends with a column
+        const bool hi16 = tid & 16, hi8 = tid & 8;
+        float a0 = hi16 ? acc[2] : acc[0], a1 = hi16 ? acc[3] : acc[1];
+        const float b0 = hi16 ? acc[0] : acc[2], b1 = hi16 ? acc[1] : acc[3];
+        a0 += __shfl_xor_sync(0xffffffffu, b0, 16);
+        a1 += __shfl_xor_sync(0xffffffffu, b1, 16);
+        const float m = hi8 ? a1 : a0, y = hi8 ? a0 : a1;
+        s_o[warp][tok][4 * cg + (hi16 ? 2 : 0) + (hi8 ? 1 : 0)] =
+            m + __shfl_xor_sync(0xffffffffu, y, 8);
+      }
+    }
+    __syncthreads();
+    if constexpr (!kState) {
+      // read before the next tile's second barrier, which comes before s_o is written again
+#pragma unroll
+      for (int i = 0; i < kTok * kCols / kSweepThreads; ++i) {
+        const int x = tid + i * kSweepThreads, tok = x / kCols, cc = x % kCols;
+        if (tok < nt && col0 + cc < w.dv) {
+          const float y = (s_o[0][tok][cc] + s_o[1][tok][cc]) + (s_o[2][tok][cc] + s_o[3][tok][cc]);
+          st1(op + g.token(p0 + tok) * w.o_t + col0 + cc, y * w.b);
+        }
+      }
+    }
+  }
+
+  if (!kState && !(g.last && w.sT)) return;
+  const float end = (w.backwards && g.n > 0) ? dec : 1.0f;
+#pragma unroll
+  for (int i = 0; i < KR; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 4 * rg + (i & 3) + 64 * (i >> 2), col = col0 + 4 * cg + j;
+      if (row >= w.dk || col >= w.dv) continue;
+      if (kState)
+        seg[static_cast<size_t>(row) * w.dv + col] = S[i][j] * end;
+      else
+        w.sT[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val] =
+            S[i][j] * end;
+    }
+}
+
+// -------------------------------------------------------------------- joining the segments
+// Every thread takes four elements of a state through the segments of its sequence.  On entry
+// slot s holds segment s's own contribution (all but the last), on exit the state before it; the
+// first one's is a copy of s0, since another block may have written sT there by then.
+__global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ LinCall c) {
+  const int blocks = (c.sw[0].dk * c.sw[0].dv / 4 + 255) / 256;
+  const LinSweep& w = c.sw[blockIdx.z];
+  const int b = static_cast<int>(blockIdx.x) / blocks, h = blockIdx.y;
+  const int e = (static_cast<int>(blockIdx.x) % blocks * 256 + static_cast<int>(threadIdx.x)) * 4;
+  int64_t first;
+  const int64_t n = lin_segments(c, b, &first);   // all threads of the block take part
+  if (n < 2 || e >= w.dk * w.dv) return;
+  const float gl = lin_power(lin_lg2(c, h), c.seg_len);
+  const int i = e / w.dv, j = e % w.dv;
+  const size_t state = static_cast<size_t>(w.dk) * w.dv;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (w.s0) {
+    const float* p = w.s0 + (static_cast<size_t>(b) * c.H + h) * state +
+                     static_cast<size_t>(i) * w.s_key + static_cast<size_t>(j) * w.s_val;
+    S = make_float4(p[0], p[w.s_val], p[2 * w.s_val], p[3 * w.s_val]);
+  }
+  float* slot = w.seg + (static_cast<size_t>(first) * c.H + h) * state + e;
+  const size_t step = static_cast<size_t>(c.H) * state;
+  float4 own = *reinterpret_cast<const float4*>(slot);
+  *reinterpret_cast<float4*>(slot) = S;
+  for (int64_t x = 1; x < n; ++x) {
+    S.x = fmaf(gl, S.x, own.x);
+    S.y = fmaf(gl, S.y, own.y);
+    S.z = fmaf(gl, S.z, own.z);
+    S.w = fmaf(gl, S.w, own.w);
+    slot += step;
+    if (x + 1 < n) own = *reinterpret_cast<const float4*>(slot);
+    *reinterpret_cast<float4*>(slot) = S;
+  }
+}
+
+// ------------------------------------------------------------------------ single token
+// Block: one sequence, one head, up to 128 columns of the state; eight warps share its rows, a
+// warp's lane holds four columns.  The state is read and written once, 16 bytes a lane and
+// contiguous along a row, with kUnroll rows in flight; everything else is small.  Bound by that
+// stream.
+constexpr int kStepThreads = 256;
+constexpr int kStepWarps = kStepThreads / 32;
+
+template <typename T>
+__device__ __forceinline__ float ld1(const T* p);
+template <>
+__device__ __forceinline__ float ld1<float>(const float* p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float ld1<__half>(const __half* p) { return __half2float(__ldg(p)); }
+
+template <typename T>
+__global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_constant__ LinStep c) {
+  constexpr int kUnroll = 8;
+  __shared__ float s_k[256], s_q[256];
+  __shared__ __align__(16) float s_o[kStepWarps][128];
+  const int64_t b = blockIdx.x;
+  const int h = blockIdx.y, col0 = static_cast<int>(blockIdx.z) * 128;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  int64_t slot = b;
+  bool skip = false;
+  if (c.slots) {
+    slot = c.slots[b];
+    // a slot named by an earlier sequence has its one update there
+    bool twice = false;
+    for (int64_t i = tid; i < b; i += kStepThreads) twice |= c.slots[i] == slot;
+    const bool out = slot < 0 || slot >= c.n_slots;
+    twice = __syncthreads_or(twice && !out);
+    skip = out || twice;
+    if ((twice || slot >= c.n_slots) && tid == 0) atomicOr(c.status, kStatusBadPlan);
+  }
+  T* op = static_cast<T*>(c.o) + b * c.o_b + h * c.o_h;
+  if (skip) {
+    if (tid < 128 && col0 + tid < c.dv) st1(op + col0 + tid, 0.0f);
+    return;
+  }
+  const T* kp = static_cast<const T*>(c.k) + b * c.k_b + h * c.k_h;
+  const T* qp = static_cast<const T*>(c.q) + b * c.q_b + h * c.q_h;
+  const T* vp = static_cast<const T*>(c.v) + b * c.v_b + h * c.v_h;
+  if (tid < c.dk) {
+    s_k[tid] = ld1<T>(kp + tid);
+    s_q[tid] = ld1<T>(qp + tid);
+  }
+  const float gamma = lin_power(lin_lg2_of(c.log_decay[h]), 1);
+  const int col = col0 + 4 * lane;
+  const bool in = col < c.dv;
+  const float4 v4 = in ? ld4<T>(vp + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float* st = c.state + (static_cast<size_t>(slot) * c.H + h) * c.dk * c.dv + col;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  for (int r0 = warp; in && r0 < c.dk; r0 += kStepWarps * kUnroll) {
+    float4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * kStepWarps;
+      if (r < c.dk) x[u] = __ldcs(reinterpret_cast<const float4*>(st + static_cast<size_t>(r) * c.dv));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * kStepWarps;
+      if (r < c.dk) {
+        const float k = s_k[r], q = s_q[r];
+        x[u].x = fmaf(k, v4.x, gamma * x[u].x);
+        x[u].y = fmaf(k, v4.y, gamma * x[u].y);
+        x[u].z = fmaf(k, v4.z, gamma * x[u].z);
+        x[u].w = fmaf(k, v4.w, gamma * x[u].w);
+        acc.x = fmaf(q, x[u].x, acc.x);
+        acc.y = fmaf(q, x[u].y, acc.y);
+        acc.z = fmaf(q, x[u].z, acc.z);
+        acc.w = fmaf(q, x[u].w, acc.w);
+        __stcs(reinterpret_cast<float4*>(st + static_cast<size_t>(r) * c.dv), x[u]);
+      }
+    }
+  }
+  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+  __syncthreads();
+  if (tid < 128 && col0 + tid < c.dv) {
+    float y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kStepWarps; ++i) y += s_o[i][tid];
+    st1(op + col0 + tid, y * c.scale);
+  }
+}
+
+template <typename T, int KR>
+cudaError_t sweeps(const LinCall& c, cudaStream_t s) {
+  const int slices = (std::max(c.sw[0].dk, c.sw[0].dv) + kCols - 1) / kCols;
+  const dim3 grid(static_cast<unsigned>(c.n_items), static_cast<unsigned>(c.H),
+                  static_cast<unsigned>(slices * c.n_sweeps));
+  if (c.split) {
+    lin_sweep_kernel<T, KR, true><<<grid, kSweepThreads, 0, s>>>(c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if ((e = launch_lin_join(c, s)) != cudaSuccess) return e;
+  }
+  lin_sweep_kernel<T, KR, false><<<grid, kSweepThreads, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t sweeps_of(const LinCall& c, cudaStream_t s) {
+  const int d = std::max(c.sw[0].dk, c.n_sweeps > 1 ? c.sw[0].dv : 0);
+  if (d <= 64) return sweeps<T, 4>(c, s);
+  if (d <= 128) return sweeps<T, 8>(c, s);
+  return sweeps<T, 16>(c, s);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_join(const LinCall& c, cudaStream_t s) {
+  const int blocks = (c.sw[0].dk * c.sw[0].dv / 4 + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(blocks * c.B), static_cast<unsigned>(c.H),
+                  static_cast<unsigned>(c.n_sweeps));
+  lin_join_kernel<<<grid, 256, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv) {
+  return (static_cast<size_t>(n_items) * H * dk * dv * 4 + 255) / 256 * 256;
+}
+
+void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sweeps,
+              int64_t* seg_len, int64_t* n_items, int* split) {
+  (void)dk;
+  // about two blocks' worth of (segment, head, sweep) for every SM, in segments of at least 256
+  constexpr int64_t kWant = 296;
+  constexpr int64_t kMin = 256;
+  int64_t L = T * H * n_sweeps * std::max(1, dv / 128) / kWant;
+  L = std::max(kMin, (L + 127) / 128 * 128);
+  const int64_t longest = ragged ? T : T / B;
+  *split = longest > L;
+  if (!*split) L = std::max<int64_t>(longest, 1);
+  *seg_len = L;
+  *n_items = !*split ? B : ragged ? T / L + B : B * ((longest + L - 1) / L);
+}
+
+cudaError_t launch_linattn(const LinCall& c, cudaStream_t s) {
+  return c.dt == kInF16 ? sweeps_of<__half>(c, s) : sweeps_of<float>(c, s);
+}
+
+cudaError_t launch_linattn_step(const LinStep& c, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(c.B), static_cast<unsigned>(c.H),
+                  static_cast<unsigned>((c.dv + 127) / 128));
+  if (c.dt == kInF16)
+    lin_step_kernel<__half><<<grid, kStepThreads, 0, s>>>(c);
+  else
+    lin_step_kernel<float><<<grid, kStepThreads, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace mmf

@@ -1,0 +1,151 @@
+// Device-side helpers of the linear attention's sweeps: powers of a head's decay and the segment
+// that a block works on.
+#pragma once
+
+#include "linattn.cuh"
+#include "ptx.cuh"
+
+namespace mmf {
+
+// log2 of a head's decay.  Decays lie in [0, 1]: a logarithm above 0 (or not a number) counts
+// as 0, that of a decay of 0 is -inf.
+__device__ __forceinline__ double lin_lg2_of(float log_decay) {
+  return static_cast<double>(fminf(log_decay, 0.0f)) * 1.4426950408889634;
+}
+__device__ __forceinline__ double lin_lg2(const LinCall& c, int h) {
+  return lin_lg2_of(__ldg(c.log_decay + h));
+}
+// gamma^n: the exponent is multiplied in double and rounded once to float (an error of at most
+// n |log2 gamma| 2^-24 relative to the power); gamma^0 is 1 for every decay.
+__device__ __forceinline__ float lin_power(double lg2, int64_t n) {
+  return n == 0 ? 1.0f : exp2f(static_cast<float>(lg2 * static_cast<double>(n)));
+}
+
+// A head's decay token by token.  gamma rounded to float is off by up to 2^-25, the same way every
+// time, which 512 tokens would raise to 10^-5 of a state.  So the two floats around gamma take
+// turns, in proportion: their products stay within one rounding of gamma's powers.
+struct LinGamma {
+  float lo, hi, share, sum;
+  __device__ __forceinline__ explicit LinGamma(double lg2) {
+    const double g = exp2(lg2);
+    lo = __double2float_rd(g);
+    hi = __double2float_ru(g);
+    share = hi > lo ? static_cast<float>((g - lo) / (static_cast<double>(hi) - lo)) : 0.0f;
+    sum = 0.5f;
+  }
+  __device__ __forceinline__ float next() {
+    sum += share;
+    const bool up = sum >= 1.0f;
+    sum = up ? sum - 1.0f : sum;
+    return up ? hi : lo;
+  }
+};
+
+struct LinSeg {
+  bool valid;      // false: the item is past the last segment
+  bool first, last;
+  int seq;
+  int64_t begin;   // the first token taken (forwards the lowest, backwards the highest)
+  int64_t n;       // tokens
+  int step;        // +1 or -1
+  __device__ __forceinline__ int64_t token(int64_t p) const { return begin + step * p; }
+};
+
+// Bounds of a sequence.  Bounds read from the device are clamped to [0, T] and to one another, so
+// that no value of them reaches outside the tensors; a clamped one is reported.
+__device__ __forceinline__ void lin_bounds(const LinCall& c, int b, int64_t* lo, int64_t* hi,
+                                           bool* bad) {
+  if (c.cu == nullptr) {
+    const int64_t len = c.T / c.B;
+    *lo = b * len;
+    *hi = *lo + len;
+    return;
+  }
+  const int64_t x = __ldg(c.cu + b), y = __ldg(c.cu + b + 1);
+  *lo = min(max(x, static_cast<int64_t>(0)), c.T);
+  *hi = min(max(y, *lo), c.T);
+  if (x != *lo || y != *hi) *bad = true;
+}
+
+// A sequence without tokens has one (empty) segment, which passes its state on.
+__device__ __forceinline__ int64_t lin_count(const LinCall& c, int64_t len) {
+  return len <= c.seg_len ? 1 : (len + c.seg_len - 1) / c.seg_len;
+}
+
+// Number of segments of sequence b and the item of its first.  Every warp of the block works it
+// out for itself; all lanes of a warp call it together.
+__device__ __forceinline__ int64_t lin_segments(const LinCall& c, int b, int64_t* first) {
+  int64_t lo, hi;
+  bool bad = false;
+  if (c.cu == nullptr) {
+    lin_bounds(c, b, &lo, &hi, &bad);
+    const int64_t n = lin_count(c, hi - lo);
+    *first = b * n;
+    return n;
+  }
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int i = lane; i < b; i += 32) {
+    lin_bounds(c, i, &lo, &hi, &bad);
+    before += lin_count(c, hi - lo);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  lin_bounds(c, b, &lo, &hi, &bad);
+  *first = before;
+  const int64_t n = lin_count(c, hi - lo);
+  // bounds that overlap can ask for more items than the call has: those are left out
+  return max(min(n, c.n_items - before), static_cast<int64_t>(0));
+}
+
+// The segment of item x (the same for every thread of the block; all lanes of a warp together).
+__device__ __forceinline__ LinSeg lin_find(const LinCall& c, int64_t x, bool backwards) {
+  LinSeg g = {};
+  int64_t lo = 0, hi = 0, k = 0;
+  bool bad = false;
+  if (c.cu == nullptr) {
+    const int64_t per = lin_count(c, c.T / c.B);
+    g.seq = static_cast<int>(x / per);
+    k = x - g.seq * per;
+    lin_bounds(c, g.seq, &lo, &hi, &bad);
+  } else {
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    int found = -1;
+    for (int b0 = 0; b0 < c.B && found < 0; b0 += 32) {
+      int64_t n = 0;
+      if (b0 + lane < c.B) {
+        lin_bounds(c, b0 + lane, &lo, &hi, &bad);
+        n = lin_count(c, hi - lo);
+      }
+      int64_t sum = n;   // inclusive prefix sum over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + sum > x);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        found = b0 + l;
+        k = x - base - __shfl_sync(0xffffffffu, sum - n, l);
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (bad) atomicOr(c.status, kStatusBadPlan);
+    if (found < 0) return g;
+    g.seq = found;
+    lin_bounds(c, found, &lo, &hi, &bad);
+  }
+  const int64_t len = hi - lo, n = lin_count(c, len);
+  g.valid = true;
+  g.first = k == 0;
+  g.last = k == n - 1;
+  const int64_t p0 = k * c.seg_len;
+  g.n = min(c.seg_len, len - p0);
+  g.step = backwards ? -1 : 1;
+  g.begin = backwards ? hi - 1 - p0 : lo + p0;
+  return g;
+}
+
+}  // namespace mmf

@@ -9,7 +9,9 @@
 
 #include "../../include/mmf.h"
 #include "backward.cuh"
+#include "int8_linear.cuh"
 #include "kernels.cuh"
+#include "linattn.cuh"
 #include "ptx.cuh"
 
 #define MMF_EXPORT extern "C" __attribute__((visibility("default")))
@@ -24,6 +26,7 @@ namespace {
 constexpr int64_t kMaxT = 16777216;
 constexpr int64_t kMaxK = 8192;
 constexpr int64_t kMaxN = 1 << 20;
+constexpr int64_t kMaxK8 = 32768;   // 8-bit projection: 128 * 127 * 32768 < 2^31
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -454,6 +457,344 @@ MMF_EXPORT mmf_status mmf_ternary_accumulate_i32(const int8_t* A, int64_t T, int
   c.wait_limit_ns = kWaitLimitNs;
   c.w8 = w.w8;
   return from_cuda(launch_ternary_gemm(c, s));
+}
+
+// ---- 8-bit projection ----------------------------------------------------------------------
+
+namespace {
+
+mmf_status check_k8(int64_t K) {
+  return K >= 16 && K <= kMaxK8 && K % 16 == 0 ? MMF_OK : MMF_ERR_UNSUPPORTED_SHAPE;
+}
+
+mmf_status check_n8(int64_t N) {
+  return N >= 8 && N <= kMaxN && N % 8 == 0 ? MMF_OK : MMF_ERR_UNSUPPORTED_SHAPE;
+}
+
+mmf_status int8_product(const int8_t* A, const float* gamma, int64_t T, int64_t K, const int8_t* W8,
+                        const float* wscale, int64_t N, void* y, int ydt, cudaStream_t s) {
+  unsigned* status = status_ptr();
+  if (!status) return MMF_ERR_CUDA;
+  Int8Call c;
+  c.A = A;
+  c.gamma = gamma;
+  c.W8 = W8;
+  c.wscale = wscale;
+  c.T = T;
+  c.K = static_cast<int>(K);
+  c.N = static_cast<int>(N);
+  c.y = y;
+  c.out_mode = ydt == MMF_F16 ? kOutF16 : kOutF32;
+  c.status = status;
+  c.wait_limit_ns = kWaitLimitNs;
+  return from_cuda(launch_int8_linear(c, s));
+}
+
+}  // namespace
+
+MMF_EXPORT mmf_status mmf_int8_quantize_weights(const void* W, mmf_dtype wdt, int64_t N, int64_t K,
+                                                int8_t* W8, float* wscale, void* stream) {
+  if (!W || !W8 || !wscale) return MMF_ERR_INVALID_ARG;
+  if (check_dtype(wdt) != MMF_OK) return MMF_ERR_INVALID_ARG;
+  mmf_status st;
+  if ((st = check_k8(K)) != MMF_OK || (st = check_n8(N)) != MMF_OK) return st;
+  if (!aligned(W, 16) || !aligned(W8, 16) || !aligned(wscale, 4)) return MMF_ERR_ALIGNMENT;
+  return from_cuda(launch_quantize_weights_i8(W, wdt == MMF_F16 ? kInF16 : kInF32, N,
+                                              static_cast<int>(K), W8, wscale,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+MMF_EXPORT mmf_status mmf_int8_forward_quantized(const int8_t* A, const float* gamma, int64_t T,
+                                                 int64_t K, const int8_t* W8, const float* wscale,
+                                                 int64_t N, void* y, mmf_dtype ydt, void* stream) {
+  if (!A || !gamma || !W8 || !wscale || !y) return MMF_ERR_INVALID_ARG;
+  if (check_dtype(ydt) != MMF_OK) return MMF_ERR_INVALID_ARG;
+  mmf_status st;
+  if ((st = check_t(T)) != MMF_OK || (st = check_k8(K)) != MMF_OK || (st = check_n8(N)) != MMF_OK)
+    return st;
+  if (!aligned(A, 16) || !aligned(W8, 16) || !aligned(y, 16) || !aligned(gamma, 4) ||
+      !aligned(wscale, 4))
+    return MMF_ERR_ALIGNMENT;
+  return int8_product(A, gamma, T, K, W8, wscale, N, y, ydt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+MMF_EXPORT size_t mmf_int8_workspace_bytes(int64_t T, int64_t K) {
+  if (check_t(T) != MMF_OK || check_k(K) != MMF_OK) return 0;
+  return up256(static_cast<size_t>(T) * static_cast<size_t>(K)) + up256(static_cast<size_t>(T) * 4);
+}
+
+MMF_EXPORT mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
+                                       const float* norm_w, float eps, const int8_t* W8,
+                                       const float* wscale, int64_t N, void* y, mmf_dtype ydt,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !W8 || !wscale || !y) return MMF_ERR_INVALID_ARG;
+  if (check_dtype(xdt) != MMF_OK || check_dtype(ydt) != MMF_OK) return MMF_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || eps != eps || eps > 1.0f) return MMF_ERR_INVALID_ARG;
+  mmf_status st;
+  if ((st = check_t(T)) != MMF_OK || (st = check_k(K)) != MMF_OK || (st = check_n8(N)) != MMF_OK)
+    return st;
+  if (!aligned(x, 16) || !aligned(W8, 16) || !aligned(y, 16) || !aligned(wscale, 4) ||
+      (norm_w && !aligned(norm_w, 16)))
+    return MMF_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < mmf_int8_workspace_bytes(T, K)) return MMF_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MMF_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int8_t* A = static_cast<int8_t*>(ws);
+  float* gamma = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                          up256(static_cast<size_t>(T) * static_cast<size_t>(K)));
+  cudaError_t e = launch_act_quant(x, xdt == MMF_F16 ? kInF16 : kInF32, T, static_cast<int>(K),
+                                   norm_w, eps, A, gamma, nullptr, s);
+  if (e != cudaSuccess) return MMF_ERR_CUDA;
+  return int8_product(A, gamma, T, K, W8, wscale, N, y, ydt, s);
+}
+
+// ---- linear attention ----------------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kMaxBatch = 1 << 20;
+
+mmf_status check_heads(int64_t B, int32_t H, int32_t dk, int32_t dv) {
+  if (B < 1 || B > kMaxBatch || H < 1 || H > kMaxHeads) return MMF_ERR_UNSUPPORTED_SHAPE;
+  if (dk < 8 || dk > 256 || dk % 8 != 0 || dv < 8 || dv > 256 || dv % 8 != 0)
+    return MMF_ERR_UNSUPPORTED_SHAPE;
+  return MMF_OK;
+}
+
+// Strides of an input: not negative, whole 16-byte vectors.
+mmf_status check_strides(int64_t t, int64_t h, int dt) {
+  const int64_t v = dt == MMF_F16 ? 8 : 4;
+  if (t < 0 || h < 0) return MMF_ERR_INVALID_ARG;
+  return t % v == 0 && h % v == 0 ? MMF_OK : MMF_ERR_ALIGNMENT;
+}
+
+// Strides of an output: no two rows of d values in one place.
+mmf_status check_out_strides(int64_t t, int64_t h, int64_t nt, int64_t nh, int64_t d, int dt) {
+  mmf_status st = check_strides(t, h, dt);
+  if (st != MMF_OK) return st;
+  if ((nt > 1 && t < d) || (nh > 1 && h < d)) return MMF_ERR_INVALID_ARG;
+  return MMF_OK;
+}
+
+mmf_status check_desc(const mmf_linattn_desc* d) {
+  if (!d || !d->log_decay || check_dtype(d->dt) != MMF_OK) return MMF_ERR_INVALID_ARG;
+  if (!(d->scale == d->scale) || d->scale - d->scale != 0.0f) return MMF_ERR_INVALID_ARG;
+  mmf_status st;
+  if ((st = check_t(d->T)) != MMF_OK || (st = check_heads(d->B, d->H, d->dk, d->dv)) != MMF_OK)
+    return st;
+  if (!d->cu_seqlens && d->T % d->B != 0) return MMF_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(d->log_decay, 4) || (d->cu_seqlens && !aligned(d->cu_seqlens, 4)))
+    return MMF_ERR_ALIGNMENT;
+  if ((st = check_strides(d->q_t, d->q_h, d->dt)) != MMF_OK ||
+      (st = check_strides(d->k_t, d->k_h, d->dt)) != MMF_OK ||
+      (st = check_strides(d->v_t, d->v_h, d->dt)) != MMF_OK ||
+      (st = check_out_strides(d->o_t, d->o_h, d->T, d->H, d->dv, d->dt)) != MMF_OK)
+    return st;
+  return MMF_OK;
+}
+
+void lin_call(const mmf_linattn_desc* d, int n_sweeps, LinCall* c) {
+  c->n_sweeps = n_sweeps;
+  c->dt = d->dt == MMF_F16 ? kInF16 : kInF32;
+  c->T = d->T;
+  c->B = static_cast<int>(d->B);
+  c->H = d->H;
+  c->cu = d->cu_seqlens;
+  c->log_decay = d->log_decay;
+  lin_plan(d->T, d->B, d->cu_seqlens != nullptr, d->H, d->dk, d->dv, n_sweeps, &c->seg_len,
+           &c->n_items, &c->split);
+}
+
+size_t lin_ws_bytes(const mmf_linattn_desc* d, int n_sweeps) {
+  if (!d || check_t(d->T) != MMF_OK || check_heads(d->B, d->H, d->dk, d->dv) != MMF_OK) return 0;
+  if (!d->cu_seqlens && d->T % d->B != 0) return 0;
+  LinCall c = {};
+  lin_call(d, n_sweeps, &c);
+  return c.split ? n_sweeps * lin_seg_bytes(c.n_items, d->H, d->dk, d->dv) : 0;
+}
+
+mmf_status lin_workspace(const mmf_linattn_desc* d, void* ws, size_t ws_bytes, LinCall* c) {
+  const size_t need = lin_ws_bytes(d, c->n_sweeps);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return MMF_ERR_WORKSPACE;
+  if (ws == nullptr && ws_bytes != 0) return MMF_ERR_WORKSPACE;
+  if (ws != nullptr && !aligned(ws, 256)) return MMF_ERR_ALIGNMENT;
+  for (int i = 0; i < c->n_sweeps; ++i)
+    c->sw[i].seg = need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                                       i * (need / c->n_sweeps))
+                            : nullptr;
+  return MMF_OK;
+}
+
+}  // namespace
+
+MMF_EXPORT size_t mmf_linattn_workspace_bytes(const mmf_linattn_desc* d) {
+  return lin_ws_bytes(d, 1);
+}
+
+MMF_EXPORT size_t mmf_linattn_backward_workspace_bytes(const mmf_linattn_desc* d) {
+  return lin_ws_bytes(d, 3);
+}
+
+MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* d, const void* q, const void* k,
+                                          const void* v, const float* h0, void* o, float* hT,
+                                          void* ws, size_t ws_bytes, void* stream) {
+  if (!q || !k || !v || !o) return MMF_ERR_INVALID_ARG;
+  mmf_status st = check_desc(d);
+  if (st != MMF_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+      (h0 && !aligned(h0, 16)) || (hT && !aligned(hT, 16)))
+    return MMF_ERR_ALIGNMENT;
+  LinCall c = {};
+  lin_call(d, 1, &c);
+  LinSweep& w = c.sw[0];
+  w.q = q;
+  w.k = k;
+  w.v = v;
+  w.o = o;
+  w.q_t = d->q_t;
+  w.q_h = d->q_h;
+  w.k_t = d->k_t;
+  w.k_h = d->k_h;
+  w.v_t = d->v_t;
+  w.v_h = d->v_h;
+  w.o_t = d->o_t;
+  w.o_h = d->o_h;
+  w.dk = d->dk;
+  w.dv = d->dv;
+  w.a = 1.0f;
+  w.b = d->scale;
+  w.s0 = h0;
+  w.sT = hT;
+  w.s_key = d->dv;
+  w.s_val = 1;
+  if ((st = lin_workspace(d, ws, ws_bytes, &c)) != MMF_OK) return st;
+  if (!(c.status = status_ptr())) return MMF_ERR_CUDA;
+  return from_cuda(launch_linattn(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+MMF_EXPORT mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void* q, const void* k,
+                                           const void* v, const void* dout, const float* h0,
+                                           const float* dhT, void* dq, void* dk, void* dv,
+                                           float* dh0, void* ws, size_t ws_bytes, void* stream) {
+  if (!q || !k || !v || !dout || !dq || !dk || !dv) return MMF_ERR_INVALID_ARG;
+  if (dh0 && dh0 == dhT) return MMF_ERR_INVALID_ARG;
+  mmf_status st = check_desc(d);
+  if (st != MMF_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || (h0 && !aligned(h0, 16)) ||
+      (dhT && !aligned(dhT, 16)) || (dh0 && !aligned(dh0, 16)))
+    return MMF_ERR_ALIGNMENT;
+  LinCall c = {};
+  lin_call(d, 3, &c);
+  const int64_t kt = static_cast<int64_t>(d->H) * d->dk, vt = static_cast<int64_t>(d->H) * d->dv;
+  // dq: forwards with the state's two sides exchanged, o -> dq, (q, k, v) -> (dout, v, k)
+  LinSweep& a = c.sw[0];
+  a.q = dout;
+  a.q_t = d->o_t;
+  a.q_h = d->o_h;
+  a.k = v;
+  a.k_t = d->v_t;
+  a.k_h = d->v_h;
+  a.v = k;
+  a.v_t = d->k_t;
+  a.v_h = d->k_h;
+  a.o = dq;
+  a.o_t = kt;
+  a.o_h = d->dk;
+  a.dk = d->dv;
+  a.dv = d->dk;
+  a.a = 1.0f;
+  a.b = d->scale;
+  a.s0 = h0;
+  a.s_key = 1;
+  a.s_val = d->dv;
+  // dk: backwards over the gradient of the state, exchanged, (q, k, v) -> (v, dout, q)
+  LinSweep& b = c.sw[1];
+  b.q = v;
+  b.q_t = d->v_t;
+  b.q_h = d->v_h;
+  b.k = dout;
+  b.k_t = d->o_t;
+  b.k_h = d->o_h;
+  b.v = q;
+  b.v_t = d->q_t;
+  b.v_h = d->q_h;
+  b.o = dk;
+  b.o_t = kt;
+  b.o_h = d->dk;
+  b.dk = d->dv;
+  b.dv = d->dk;
+  b.a = d->scale;
+  b.b = 1.0f;
+  b.backwards = 1;
+  b.s0 = dhT;
+  b.s_key = 1;
+  b.s_val = d->dv;
+  // dv: the same gradient of the state, (q, k, v) -> (k, q, dout); its last value is dh0
+  LinSweep& e = c.sw[2];
+  e.q = k;
+  e.q_t = d->k_t;
+  e.q_h = d->k_h;
+  e.k = q;
+  e.k_t = d->q_t;
+  e.k_h = d->q_h;
+  e.v = dout;
+  e.v_t = d->o_t;
+  e.v_h = d->o_h;
+  e.o = dv;
+  e.o_t = vt;
+  e.o_h = d->dv;
+  e.dk = d->dk;
+  e.dv = d->dv;
+  e.a = d->scale;
+  e.b = 1.0f;
+  e.backwards = 1;
+  e.s0 = dhT;
+  e.sT = dh0;
+  e.s_key = d->dv;
+  e.s_val = 1;
+  if ((st = lin_workspace(d, ws, ws_bytes, &c)) != MMF_OK) return st;
+  if (!(c.status = status_ptr())) return MMF_ERR_CUDA;
+  return from_cuda(launch_linattn(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+MMF_EXPORT mmf_status mmf_linattn_step(const mmf_linattn_desc* d, const void* q, const void* k,
+                                       const void* v, void* o, float* state, const int32_t* slots,
+                                       int64_t n_slots, void* stream) {
+  if (!q || !k || !v || !o || !state) return MMF_ERR_INVALID_ARG;
+  mmf_status st = check_desc(d);
+  if (st != MMF_OK) return st;
+  if (d->cu_seqlens || d->T != d->B) return MMF_ERR_INVALID_ARG;
+  if (slots ? (n_slots < 1 || n_slots > kMaxBatch) : n_slots != 0) return MMF_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+      !aligned(state, 16) || (slots && !aligned(slots, 4)))
+    return MMF_ERR_ALIGNMENT;
+  LinStep c = {};
+  c.q = q;
+  c.k = k;
+  c.v = v;
+  c.o = o;
+  c.q_b = d->q_t;
+  c.q_h = d->q_h;
+  c.k_b = d->k_t;
+  c.k_h = d->k_h;
+  c.v_b = d->v_t;
+  c.v_h = d->v_h;
+  c.o_b = d->o_t;
+  c.o_h = d->o_h;
+  c.dt = d->dt == MMF_F16 ? kInF16 : kInF32;
+  c.B = d->B;
+  c.H = d->H;
+  c.dk = d->dk;
+  c.dv = d->dv;
+  c.log_decay = d->log_decay;
+  c.scale = d->scale;
+  c.state = state;
+  c.slots = slots;
+  c.n_slots = n_slots;
+  if (!(c.status = status_ptr())) return MMF_ERR_CUDA;
+  return from_cuda(launch_linattn_step(c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 MMF_EXPORT mmf_status mmf_get_device_status(void) {
