@@ -8,8 +8,9 @@
 // Splitting.  A sweep is serial in the tokens, so when (sequence, head) pairs are too few to fill
 // the GPU every sequence is cut into segments of L tokens: one pass finds each segment's own
 // contribution to the state from k and v alone (kState), a second joins them,
-//   start_{s+1} = gamma^L start_s + own_s,
-// and the third runs all segments at once from their start states.
+//   start_{s+1} = gamma^(tokens of s) start_s + own_s,
+// which also gives the state after the last, and the third runs all segments at once from their
+// start states.  A sequence of one segment is left to the third alone.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
   if (col0 >= w.dv) return;
   const int h = blockIdx.y;
   const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
-  if (!g.valid || (kState && (g.last || g.n == 0))) return;
+  const bool whole = g.first && g.last;   // an unsplit sequence: nothing to start from
+  if (!g.valid || (kState && whole)) return;
 
   const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3, warp = tid >> 5;
   LinGamma gamma(lin_lg2(c, h));
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
       const int row = 4 * rg + (i & 3) + 64 * (i >> 2), col = col0 + 4 * cg + j;
       float x = 0.0f;
       if (!kState && row < w.dk && col < w.dv) {
-        if (c.split && !(g.first && g.last))   // one segment: nothing was joined
+        if (c.split && !whole)
           x = seg[static_cast<size_t>(row) * w.dv + col];
         else if (w.s0)
           x = w.s0[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val];
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
     }
   }
 
-  if (!kState && !(g.last && w.sT)) return;
+  if (!kState && !(whole && w.sT)) return;
   const float end = (w.backwards && g.n > 0) ? dec : 1.0f;
 #pragma unroll
   for (int i = 0; i < KR; ++i)
@@ -195,37 +197,58 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
 
 // -------------------------------------------------------------------- joining the segments
 // Every thread takes four elements of a state through the segments of its sequence.  On entry
-// slot s holds segment s's own contribution (all but the last), on exit the state before it; the
-// first one's is a copy of s0, since another block may have written sT there by then.
+// slot s holds segment s's own contribution, on exit the state before it; sT gets the state after
+// the last.  The first slot becomes a copy of s0, which may be sT itself.
 __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ LinCall c) {
   const int blocks = (c.sw[0].dk * c.sw[0].dv / 4 + 255) / 256;
   const LinSweep& w = c.sw[blockIdx.z];
   const int b = static_cast<int>(blockIdx.x) / blocks, h = blockIdx.y;
   const int e = (static_cast<int>(blockIdx.x) % blocks * 256 + static_cast<int>(threadIdx.x)) * 4;
-  int64_t first;
-  const int64_t n = lin_segments(c, b, &first);   // all threads of the block take part
+  int64_t first, len;
+  const int64_t n = lin_segments(c, b, &first, &len);   // whole warps
   if (n < 2 || e >= w.dk * w.dv) return;
-  const float gl = lin_power(lin_lg2(c, h), c.seg_len);
+  const double lg2 = lin_lg2(c, h);
+  const float gl = lin_power(lg2, c.seg_len);
+  const float glast = lin_power(lg2, max(len - (n - 1) * c.seg_len, static_cast<int64_t>(0)));
   const int i = e / w.dv, j = e % w.dv;
   const size_t state = static_cast<size_t>(w.dk) * w.dv;
+  const size_t at = (static_cast<size_t>(b) * c.H + h) * state + static_cast<size_t>(i) * w.s_key +
+                    static_cast<size_t>(j) * w.s_val;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (w.s0) {
-    const float* p = w.s0 + (static_cast<size_t>(b) * c.H + h) * state +
-                     static_cast<size_t>(i) * w.s_key + static_cast<size_t>(j) * w.s_val;
+    const float* p = w.s0 + at;
     S = make_float4(p[0], p[w.s_val], p[2 * w.s_val], p[3 * w.s_val]);
   }
   float* slot = w.seg + (static_cast<size_t>(first) * c.H + h) * state + e;
   const size_t step = static_cast<size_t>(c.H) * state;
-  float4 own = *reinterpret_cast<const float4*>(slot);
-  *reinterpret_cast<float4*>(slot) = S;
-  for (int64_t x = 1; x < n; ++x) {
-    S.x = fmaf(gl, S.x, own.x);
-    S.y = fmaf(gl, S.y, own.y);
-    S.z = fmaf(gl, S.z, own.z);
-    S.w = fmaf(gl, S.w, own.w);
-    slot += step;
-    if (x + 1 < n) own = *reinterpret_cast<const float4*>(slot);
-    *reinterpret_cast<float4*>(slot) = S;
+  constexpr int kAhead = 4;   // slots in flight
+  float4 own[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < n) own[u] = *reinterpret_cast<const float4*>(slot + u * step);
+  for (int64_t x0 = 0; x0 < n; x0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t x = x0 + u;
+      if (x < n) {
+        const float4 o = own[u];
+        if (x + kAhead < n) own[u] = *reinterpret_cast<const float4*>(slot + kAhead * step);
+        *reinterpret_cast<float4*>(slot) = S;
+        slot += step;
+        const float f = x + 1 < n ? gl : glast;
+        S.x = fmaf(f, S.x, o.x);
+        S.y = fmaf(f, S.y, o.y);
+        S.z = fmaf(f, S.z, o.z);
+        S.w = fmaf(f, S.w, o.w);
+      }
+    }
+  }
+  if (w.sT) {
+    float* p = w.sT + at;
+    p[0] = S.x;
+    p[w.s_val] = S.y;
+    p[2 * w.s_val] = S.z;
+    p[3 * w.s_val] = S.w;
   }
 }
 
@@ -371,6 +394,7 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sw
 }
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s) {
+  if (lin_mma_supported(c)) return launch_lin_mma(c, s);
   return c.dt == kInF16 ? sweeps_of<__half>(c, s) : sweeps_of<float>(c, s);
 }
 

@@ -55,6 +55,10 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sw
 size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv);
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s);
+
+// The same on the tensor cores: fp16, every dk 64 or 128, every dv a multiple of 64.
+bool lin_mma_supported(const LinCall& c);
+cudaError_t launch_lin_mma(const LinCall& c, cudaStream_t s);
 // The second pass of a split: every segment's start state from the segments' own contributions.
 cudaError_t launch_lin_join(const LinCall& c, cudaStream_t s);
 

@@ -72,15 +72,17 @@ __device__ __forceinline__ int64_t lin_count(const LinCall& c, int64_t len) {
   return len <= c.seg_len ? 1 : (len + c.seg_len - 1) / c.seg_len;
 }
 
-// Number of segments of sequence b and the item of its first.  Every warp of the block works it
+// Number of segments of sequence b, the item of its first and its length.  Every warp of the block works it
 // out for itself; all lanes of a warp call it together.
-__device__ __forceinline__ int64_t lin_segments(const LinCall& c, int b, int64_t* first) {
+__device__ __forceinline__ int64_t lin_segments(const LinCall& c, int b, int64_t* first,
+                                                int64_t* len) {
   int64_t lo, hi;
   bool bad = false;
   if (c.cu == nullptr) {
     lin_bounds(c, b, &lo, &hi, &bad);
     const int64_t n = lin_count(c, hi - lo);
     *first = b * n;
+    *len = hi - lo;
     return n;
   }
   const int lane = threadIdx.x & 31;
@@ -93,6 +95,7 @@ __device__ __forceinline__ int64_t lin_segments(const LinCall& c, int b, int64_t
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   lin_bounds(c, b, &lo, &hi, &bad);
   *first = before;
+  *len = hi - lo;
   const int64_t n = lin_count(c, hi - lo);
   // bounds that overlap can ask for more items than the call has: those are left out
   return max(min(n, c.n_items - before), static_cast<int64_t>(0));
