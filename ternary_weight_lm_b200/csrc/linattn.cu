@@ -378,15 +378,24 @@ size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv) {
   return (static_cast<size_t>(n_items) * H * dk * dv * 4 + 255) / 256 * 256;
 }
 
-void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sweeps,
+void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split) {
-  (void)dk;
-  // about two blocks' worth of (segment, head, sweep) for every SM, in segments of at least 256
-  constexpr int64_t kWant = 296;
+  // Segments that run at once on 148 SMs: one block for a head on an SM with tcgen05, two to four
+  // on it otherwise (by the registers of a state).  A block per segment, head, sweep and tile of
+  // columns; segments are whole chunks and at least 256 tokens, below which reading k and v twice
+  // and passing states through memory costs more than the blocks that it adds.
   constexpr int64_t kMin = 256;
-  int64_t L = T * H * n_sweeps * std::max(1, dv / 128) / kWant;
-  L = std::max(kMin, (L + 127) / 128 * 128);
+  const bool half = dt == kInF16;
+  const bool tc = half && dk == 128 && dv == 128;
+  const int64_t slots = 148 * (tc ? 1 : half && std::min(dk, dv) <= 64 ? 4 : 2);
+  const int64_t width = tc ? 1 : std::max(1, dv / (half ? 128 : 64));
+  const int64_t units = std::max<int64_t>(1, H * n_sweeps * width);
   const int64_t longest = ragged ? T : T / B;
+  // segments of all sequences together, at most one wave of blocks
+  const int64_t all = std::max<int64_t>(1, slots / units);
+  const int64_t per = ragged ? all : std::max<int64_t>(1, all / B);
+  int64_t L = (longest + per - 1) / per;
+  L = std::max(kMin, (L + 127) / 128 * 128);
   *split = longest > L;
   if (!*split) L = std::max<int64_t>(longest, 1);
   *seg_len = L;
@@ -394,6 +403,7 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sw
 }
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s) {
+  if (lin_tc_supported(c)) return launch_lin_tc(c, s);
   if (lin_mma_supported(c)) return launch_lin_mma(c, s);
   return c.dt == kInF16 ? sweeps_of<__half>(c, s) : sweeps_of<float>(c, s);
 }

@@ -48,9 +48,9 @@ struct LinCall {
   unsigned* status;
 };
 
-// Segment length for a call of these sizes (a function of sizes alone), the number of items and
-// whether the sequences are split.
-void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int n_sweeps,
+// Segment length for a call of these sizes and type (a function of them alone), the number of
+// items and whether the sequences are split.
+void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split);
 size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv);
 
@@ -61,6 +61,10 @@ bool lin_mma_supported(const LinCall& c);
 cudaError_t launch_lin_mma(const LinCall& c, cudaStream_t s);
 // The second pass of a split: every segment's start state from the segments' own contributions.
 cudaError_t launch_lin_join(const LinCall& c, cudaStream_t s);
+
+// And with tcgen05: fp16 heads of 128 x 128.
+bool lin_tc_supported(const LinCall& c);
+cudaError_t launch_lin_tc(const LinCall& c, cudaStream_t s);
 
 // One token of each sequence: state [rows x H x dk x dv] updated in place, o = scale S^T q.
 // q, k, v, o: [B x H x d] with strides of a sequence and of a head.  slots (or nullptr: row b is

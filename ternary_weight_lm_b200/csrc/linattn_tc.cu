@@ -1,0 +1,692 @@
+// Linear attention with a decay for each head on the 5th-generation tensor cores (tcgen05,
+// kind::f16): fp16 heads of 128 x 128, chunks of 128 tokens, one block on an SM.
+//
+// The arithmetic of a chunk (q_i, k_j, v_j: its tokens in the sweep's order, n of them; S the state
+// before it; lag 0 forwards, 1 backwards):
+//   P_ij  = a gamma^(i-j) q_i . k_j                     for j <= i, else 0
+//   o_i   = b (gamma^(i+1-lag) S^T q_i + sum_j P_ij v_j)
+//   S    <- gamma^n S + sum_j (a gamma^(n-1-j+lag) k_j) v_j^T
+// as four products of 128 x 128 x 128:
+//   Q K^T (both as loaded) -> P,  Q S -> o_i's first part,  P V (P from TMEM) -> its second part,
+//   V^T K' with K' the decayed K (contracted over the tokens: both operands "MN-major").
+// All operands sit in shared memory as the 128-byte-swizzled tiles that TMA writes, so the same
+// image of K serves Q K^T (K-major) and V^T K' (MN-major), and V likewise.
+//
+// Warps: 0 TMA, 1 TMEM and MMA issue, 2-5 the state's (thread = column of v = row of S^T, whose 128
+// values stay in its registers; also K -> K'), 6-9 the rows' (thread = token: scores and outputs).
+// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' is carried as two
+// fp16 parts (22 bits), since the state is an fp32 output: the first overwrites K once Q K^T is
+// done, the second overwrites Q once Q S is done as well.  TMEM: P, Q S, P V, V^T K', 128 columns
+// each; the fp16 P overwrites P.
+//
+// Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
+// K' scaled by powers of two (a row's, the state's, the chunk's) before they are rounded.  The
+// state adds a chunk's product by one fp32 operation.
+//
+// A v that is not finite would reach earlier tokens through P V as 0 times infinity.  Such values
+// are replaced by zero on arrival and their place is noted: from that token on the column's
+// outputs and state are NaN.
+//
+// kState: the state alone (pass one of a split sequence).  There the row warps turn K into K'
+// while the state warps add the chunk before.
+//
+// Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
+// copies and MMAs in flight are drained and TMEM is freed.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "linattn.cuh"
+#include "linattn_dev.cuh"
+#include "ptx.cuh"
+
+namespace mmf {
+namespace {
+
+constexpr int kD = 128;                      // head size, k and v
+constexpr int kC = 128;                      // tokens of a chunk
+constexpr int kPanel = kC * 128;             // 128 rows x 64 fp16
+constexpr int kTile = 2 * kPanel;            // 32 KB
+constexpr int kThreads = 320;
+constexpr int kGroup = 128;                  // threads of the state warps, and of the row warps
+constexpr uint64_t kDrainNs = 2000000000ull;
+
+template <bool kState>
+struct Lay {
+  static constexpr int kStages = 2;
+  static constexpr int kStage = 3 * kTile;   // K, V, Q (kState: room for the second part of K')
+  static constexpr int kS = kStages * kStage;
+  static constexpr int kSmem = 1024 + kS + (kState ? 0 : kTile);
+  static constexpr int kCols = kState ? 128 : 512;
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// kind::f16, fp32 accumulator, fp16 operands, M = N = 128; bits 15 and 16: A and B MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((kD / 8) << 17) |
+         ((kC / 16) << 24);
+}
+
+// Descriptor of an MN-major operand: 64 values of M or N are the 128 bytes of a swizzled row, the
+// contraction runs over the rows.  Leading offset: to the next 64 values (the second panel);
+// stride offset: to the next eight rows.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(kPanel >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Both K-major: contraction over the 64 + 64 values of the two panels' rows.
+__device__ __forceinline__ void product_kk(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = idesc_f16(false, false);
+  const uint64_t ad = smem_desc_kmajor_sw128(a), bd = smem_desc_kmajor_sw128(b);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t off = static_cast<uint64_t>(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
+    mma_ss(d, ad + off, bd + off, idesc, k > 0 ? 1u : 0u);
+  }
+}
+// Both MN-major: contraction over the tiles' 128 rows.
+__device__ __forceinline__ void product_mn(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t idesc = idesc_f16(true, true);
+  const uint64_t ad = desc_mn(a), bd = desc_mn(b);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t off = static_cast<uint64_t>((k * 16 * 128) >> 4);
+    mma_ss(d, ad + off, bd + off, idesc, (k > 0 || add) ? 1u : 0u);
+  }
+}
+// A in TMEM (16 fp16 are eight columns), B MN-major.
+__device__ __forceinline__ void product_tm(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = idesc_f16(false, true);
+  const uint64_t bd = desc_mn(b);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_ts(d, a + 8u * k, bd + static_cast<uint64_t>((k * 16 * 128) >> 4), idesc, k > 0 ? 1u : 0u);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Exponent of the power of two that brings a magnitude (as bits) to 2^14 .. 2^15; zeros take none.
+__device__ __forceinline__ int up_to_half(uint32_t bits) {
+  return bits == 0u ? 0 : max(-100, min(14 + 127 - static_cast<int>(bits >> 23), 100));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// 16-byte vector x (0..15) of row r of a two-panel tile
+__device__ __forceinline__ uint32_t vec_at(uint32_t tile, int r, int x) {
+  return tile + static_cast<uint32_t>((x >> 3) * kPanel + r * 128 + (((x & 7) ^ (r & 7)) << 4));
+}
+
+// Tensor maps of each sweep's k, v and q.
+struct LinMaps {
+  CUtensorMap m[3 * kMaxSweeps];
+};
+
+struct Bars {
+  uint64_t full[2], empty[2];
+  uint64_t scores, qk, p, v, k, out, drained, upd, state, drain;
+};
+
+struct Shared {
+  Bars bars;
+  float pow[kC + 1];        // gamma^0 .. gamma^128
+  uint32_t red_k[4], red_s[4];
+  int exp_s[2];             // exponent of the fp16 state, by chunk parity
+  int exp_k[2];             // of K'
+  int bad_at[kD];           // first position of the segment whose v is not finite, by column
+  int any_bad;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(Lay<false>::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory per block");
+
+template <bool kState>
+__global__ void __launch_bounds__(kThreads, 1)
+lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps maps) {
+  using L = Lay<kState>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  auto tile_k = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage); };
+  auto tile_v = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage + kTile); };
+  auto tile_q = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage + 2 * kTile); };
+  const uint32_t tile_s = base + static_cast<uint32_t>(L::kS);
+
+  const int sweep = blockIdx.z, h = blockIdx.y;
+  const LinSweep& w = c.sw[sweep];
+  const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
+  const bool whole = g.first && g.last;
+  if (!g.valid || (kState && whole)) return;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool back = w.backwards != 0;
+  const int lag = back ? 1 : 0;
+  const int chunks = static_cast<int>((g.n + kC - 1) / kC);
+  const CUtensorMap* mk = &maps.m[3 * sweep];
+  const CUtensorMap* mv = &maps.m[3 * sweep + 1];
+  const CUtensorMap* mq = &maps.m[3 * sweep + 2];
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sh.bars.full[s]), 1);
+      mbar_init(smem_u32(&sh.bars.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh.bars.scores), 1);
+    mbar_init(smem_u32(&sh.bars.qk), 1);
+    mbar_init(smem_u32(&sh.bars.p), 4);
+    mbar_init(smem_u32(&sh.bars.v), 4);
+    mbar_init(smem_u32(&sh.bars.k), 4);
+    mbar_init(smem_u32(&sh.bars.out), 1);
+    mbar_init(smem_u32(&sh.bars.drained), 4);
+    mbar_init(smem_u32(&sh.bars.upd), 1);
+    mbar_init(smem_u32(&sh.bars.state), 4);
+    mbar_init(smem_u32(&sh.bars.drain), 1);
+    sh.abort = 0;
+    sh.any_bad = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(mk);
+    tma_prefetch_desc(mv);
+    if (!kState) tma_prefetch_desc(mq);
+  }
+  if (tid <= kC) sh.pow[tid] = lin_power(lin_lg2(c, h), tid);
+  if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), L::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t t_p = tmem, t_qs = tmem + 128, t_pv = tmem + 256, t_upd = tmem + (kState ? 0 : 384);
+  volatile int* abort_flag = &sh.abort;
+  // waits of a whole warp, with one outcome
+  auto wait = [&](uint64_t& bar, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), static_cast<uint32_t>(parity),
+                                                     kWaitLimitNs, abort_flag, c.status));
+  };
+  auto arrive = [&](uint64_t& bar) {   // once for the warp, after all its lanes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
+  };
+  // first token row of a chunk's tile: rows ascend with the tokens in both directions
+  auto row0 = [&](int chunk) {
+    return g.begin + (back ? -(static_cast<int64_t>(chunk) * kC + kC - 1) : static_cast<int64_t>(chunk) * kC);
+  };
+  auto tokens = [&](int chunk) {
+    return static_cast<int>(min(static_cast<int64_t>(kC), g.n - static_cast<int64_t>(chunk) * kC));
+  };
+
+  // Thread r of a group of four warps (named barrier `id`): row r of V made safe for the products:
+  // zeros where the row is no token of the segment and where a value is not finite.
+  auto clean_v = [&](int chunk, int r) {
+    const int s = chunk & 1, pos = back ? kC - 1 - r : r;
+    const uint32_t t = tile_v(s);
+    if (pos >= tokens(chunk)) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) sts128(vec_at(t, r, x), make_uint4(0u, 0u, 0u, 0u));
+    } else {
+      uint32_t odd = 0u;   // an exponent of all ones carries into its sign's place
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const uint4 v = lds128(vec_at(t, r, x));
+        odd |= ((v.x & 0x7c007c00u) + 0x04000400u) | ((v.y & 0x7c007c00u) + 0x04000400u) |
+               ((v.z & 0x7c007c00u) + 0x04000400u) | ((v.w & 0x7c007c00u) + 0x04000400u);
+      }
+      if (odd & 0x80008000u) {
+        for (int col = 0; col < kD; ++col) {
+          const uint32_t a = vec_at(t, r, col >> 3) + 2u * (col & 7);
+          uint16_t x;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+          if ((x & 0x7c00u) == 0x7c00u) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
+            atomicMin(&sh.bad_at[col], chunk * kC + pos);
+            sh.any_bad = 1;
+          }
+        }
+      }
+    }
+    fence_proxy_async_smem();
+  };
+  // Row r of K' from row r of K: a gamma^(tokens after it) k_j in two fp16 parts, scaled by the
+  // chunk's power of two.  False if one of the group's warps gave up (`ok`).
+  auto decay_k = [&](int chunk, int r, int id, bool ok) {
+    const int s = chunk & 1, n = tokens(chunk), pos = back ? kC - 1 - r : r;
+    const uint32_t t = tile_k(s), t2 = tile_q(s);
+    const bool in = pos < n;
+    const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
+    __half2 m2 = __float2half2_rn(0.0f);
+    if (ok) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const uint4 v = lds128(vec_at(t, r, x));
+        const __half2* hv = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m2 = __hmax2(m2, __habs2(hv[e]));
+      }
+    }
+    uint32_t top = 0u;
+    if (in) top = max(magnitude(__low2float(m2) * wt), magnitude(__high2float(m2) * wt));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) sh.red_k[r >> 5] = top;
+    if (!named_bar_and(id, kGroup, ok)) return false;
+    const int e = up_to_half(max(max(sh.red_k[0], sh.red_k[1]), max(sh.red_k[2], sh.red_k[3])));
+    if (r == 0) sh.exp_k[s] = e;
+    const float f = wt * pow2(e);
+#pragma unroll 4
+    for (int x = 0; x < 16; ++x) {
+      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+      if (in) {
+        const uint4 v = lds128(vec_at(t, r, x));
+        const uint32_t* vi = reinterpret_cast<const uint32_t*>(&v);
+        uint32_t* ho = reinterpret_cast<uint32_t*>(&hi);
+        uint32_t* lo_ = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 y = unpack2(vi[i]);
+          y.x *= f;
+          y.y *= f;
+          ho[i] = pack2(y.x, y.y);
+          const float2 z = unpack2(ho[i]);
+          lo_[i] = pack2(y.x - z.x, y.y - z.y);
+        }
+      }
+      sts128(vec_at(t, r, x), hi);
+      sts128(vec_at(t2, r, x), lo);
+    }
+    fence_proxy_async_smem();
+    return true;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------------ TMA
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      auto col = [&](int64_t stride) { return static_cast<int32_t>(h * stride); };
+      int issued = 0;
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int s = ch & 1;
+        if (ch >= 2 && !mbar_wait_bounded(smem_u32(&sh.bars.empty[s]), ((ch >> 1) - 1) & 1,
+                                          kWaitLimitNs, abort_flag, c.status))
+          break;
+        const uint32_t bar = smem_u32(&sh.bars.full[s]);
+        mbar_arrive_expect_tx(bar, (kState ? 2 : 3) * kTile);
+        const int32_t y = static_cast<int32_t>(row0(ch));
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (!kState) tma_load_2d(tile_q(s) + p * kPanel, mq, bar, col(w.q_h) + 64 * p, y, pol);
+          tma_load_2d(tile_k(s) + p * kPanel, mk, bar, col(w.k_h) + 64 * p, y, pol);
+          tma_load_2d(tile_v(s) + p * kPanel, mv, bar, col(w.v_h) + 64 * p, y, pol);
+        }
+        issued = ch + 1;
+      }
+      for (int ch = issued > 2 ? issued - 2 : 0; ch < issued; ++ch)   // all land before the block ends
+        mbar_wait_bounded(smem_u32(&sh.bars.full[ch & 1]), (ch >> 1) & 1, kDrainNs, nullptr, c.status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------------ MMA
+    auto commit = [&](uint64_t& bar) { tc_commit_warp(smem_u32(&bar)); };
+    if constexpr (kState) {
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int s = ch & 1;
+        // K' and V are ready, and the update before is read
+        if (!wait(sh.bars.k, ch & 1)) break;
+        if (ch > 0 && !wait(sh.bars.state, (ch - 1) & 1)) break;
+        tc_fence_after();
+        product_mn(t_upd, tile_v(s), tile_k(s), false);
+        product_mn(t_upd, tile_v(s), tile_q(s), true);
+        commit(sh.bars.upd);
+        commit(sh.bars.empty[s]);
+      }
+    } else {
+      bool ok = true;
+      for (int ch = 0; ok && ch < chunks; ++ch) {
+        const int s = ch & 1;
+        // scores, in P's place: the product that read it last has completed
+        ok = wait(sh.bars.full[s], (ch >> 1) & 1) && (ch == 0 || wait(sh.bars.out, (ch - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        product_kk(t_p, tile_q(s), tile_k(s));
+        commit(sh.bars.scores);
+        // Q S: the state is in shared memory, and the outputs before are read
+        ok = wait(sh.bars.state, ch & 1) && (ch == 0 || wait(sh.bars.drained, (ch - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        product_kk(t_qs, tile_q(s), tile_s);
+        commit(sh.bars.qk);
+        ok = wait(sh.bars.v, ch & 1) && wait(sh.bars.p, ch & 1);
+        if (!ok) break;
+        tc_fence_after();
+        product_tm(t_pv, t_p, tile_v(s));
+        commit(sh.bars.out);
+        ok = wait(sh.bars.k, ch & 1);
+        if (!ok) break;
+        tc_fence_after();
+        product_mn(t_upd, tile_v(s), tile_k(s), false);
+        product_mn(t_upd, tile_v(s), tile_q(s), true);
+        commit(sh.bars.upd);
+        commit(sh.bars.empty[s]);
+      }
+    }
+    commit(sh.bars.drain);
+    mbar_wait_bounded(smem_u32(&sh.bars.drain), 0, kDrainNs, nullptr, c.status);
+    __syncwarp();
+  } else if (warp < 6) {
+    // ------------------------------------------------------------------------------ state
+    const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: row of S^T
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
+    const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * kD * kD;
+    float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * kD * kD : nullptr;
+    float S[kD];
+    {
+      const float* from = nullptr;
+      size_t sk = kD, sv = 1;
+      if (!kState && c.split && !whole) {
+        from = seg;
+      } else if (!kState && w.s0) {
+        from = w.s0 + state0;
+        sk = static_cast<size_t>(w.s_key);
+        sv = static_cast<size_t>(w.s_val);
+      }
+#pragma unroll
+      for (int i = 0; i < kD; ++i) S[i] = from ? from[i * sk + r * sv] : 0.0f;
+    }
+    uint32_t top = 0u;
+    if constexpr (!kState) {
+#pragma unroll
+      for (int i = 0; i < kD; ++i) top = max(top, magnitude(S[i]));
+    }
+    // the state for chunk ch: scaled, rounded and written as the B operand of Q S
+    auto publish = [&](int ch, bool ok) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) sh.red_s[q] = top;
+      if (!named_bar_and(1, kGroup, ok)) return false;
+      const int e = up_to_half(max(max(sh.red_s[0], sh.red_s[1]), max(sh.red_s[2], sh.red_s[3])));
+      if (r == 0) sh.exp_s[ch & 1] = e;
+      const float f = pow2(e);
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        sts128(vec_at(tile_s, r, x),
+               make_uint4(pack2(S[8 * x] * f, S[8 * x + 1] * f), pack2(S[8 * x + 2] * f, S[8 * x + 3] * f),
+                          pack2(S[8 * x + 4] * f, S[8 * x + 5] * f), pack2(S[8 * x + 6] * f, S[8 * x + 7] * f)));
+      fence_proxy_async_smem();
+      arrive(sh.bars.state);
+      return true;
+    };
+    bool ok = true;
+    if constexpr (!kState) ok = publish(0, true);
+    for (int ch = 0; ok && ch < chunks; ++ch) {
+      const int s = ch & 1;
+      if constexpr (!kState) {
+        bool w1 = wait(sh.bars.full[s], (ch >> 1) & 1);
+        if (w1) {
+          clean_v(ch, r);
+          arrive(sh.bars.v);
+        }
+        w1 = w1 && wait(sh.bars.qk, ch & 1);   // K and Q are no longer read as such
+        if (!decay_k(ch, r, 1, w1)) {
+          ok = false;
+          break;
+        }
+        arrive(sh.bars.k);
+      }
+      const bool w2 = wait(sh.bars.upd, ch & 1);
+      if (w2) {
+        tc_fence_after();
+        const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[s]);
+        top = 0u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t d[32];
+          tc_ld_32x32b_x32(t_upd + lane_addr + 32u * b, d);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float& x = S[32 * b + i];
+            x = fmaf(decay, x, __uint_as_float(d[i]) * f);
+            if constexpr (!kState) top = max(top, magnitude(x));
+          }
+        }
+        tc_fence_before();
+      }
+      if constexpr (kState) {
+        ok = w2;
+        if (ok) arrive(sh.bars.state);
+      } else {
+        ok = publish(ch + 1, w2);
+      }
+    }
+    ok = named_bar_and(1, kGroup, ok);
+    const bool mine = kState || (whole && w.sT != nullptr);
+    if (ok && mine) {
+      float* to = kState ? seg : w.sT + state0;
+      const size_t sk = kState ? kD : static_cast<size_t>(w.s_key);
+      const size_t sv = kState ? 1 : static_cast<size_t>(w.s_val);
+      const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) && sh.bad_at[r] != 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < kD; ++i) to[i * sk + r * sv] = bad ? __int_as_float(0x7fffffff) : S[i];
+    }
+  } else {
+    // ------------------------------------------------------------------------------- rows
+    const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: token row
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
+    if constexpr (kState) {
+      for (int ch = 0; ch < chunks; ++ch) {
+        const bool ok = wait(sh.bars.full[ch & 1], (ch >> 1) & 1);
+        if (ok) clean_v(ch, r);
+        if (!decay_k(ch, r, 2, ok)) break;
+        arrive(sh.bars.k);
+      }
+    } else {
+      const int i = back ? kC - 1 - r : r;         // place in the chunk
+      __half* op = static_cast<__half*>(w.o) + h * w.o_h;
+      const bool wide = ((reinterpret_cast<uintptr_t>(op) | static_cast<uintptr_t>(2 * w.o_t)) & 31) == 0;
+      for (int ch = 0; ch < chunks; ++ch) {
+        if (!wait(sh.bars.scores, ch & 1)) break;
+        tc_fence_after();
+        int e;
+        {
+          float P[kC];
+          uint32_t top = 0u;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            // blocks of 32 columns: before the warp's rows, across them, after them
+            const bool past = back ? b > q : b < q;
+            if (past || b == q) {
+              uint32_t d[32];
+              tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
+              tc_wait_ld();
+              // gamma^(i-j) of a whole block: a row's factor times a column's, both at most 1
+              const float rowf = past ? w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31] : w.a;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                float f;
+                if (past) {
+                  f = rowf * sh.pow[back ? j : 31 - j];
+                } else {
+                  const int d1 = back ? j - lane : lane - j;
+                  f = d1 >= 0 ? rowf * sh.pow[d1] : 0.0f;
+                }
+                // not a product with 0: the score of a later token may be anything
+                const float x = (past || (back ? j >= lane : j <= lane)) ? __uint_as_float(d[j]) * f : 0.0f;
+                P[32 * b + j] = x;
+                top = max(top, magnitude(x));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) P[32 * b + j] = 0.0f;
+            }
+          }
+          e = up_to_half(top);
+          const float f = pow2(e);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t u[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] = pack2(P[64 * b + 2 * j] * f, P[64 * b + 2 * j + 1] * f);
+            tc_st_32x32b_x32(t_p + lane_addr + 32u * b, u);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          // the state's exponent; its barrier cannot move on before P is handed over
+          if (!wait(sh.bars.state, ch & 1)) break;
+          arrive(sh.bars.p);
+        }
+        if (!wait(sh.bars.out, ch & 1)) break;
+        tc_fence_after();
+        const float fi = w.b * sh.pow[i + 1 - lag] * pow2(-sh.exp_s[ch & 1]);
+        const float fa = w.b * pow2(-e);
+        const bool in = i < tokens(ch);
+        const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
+        __half* row = op + (row0(ch) + r) * w.o_t;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t x[32], y[32];
+          tc_ld_32x32b_x32(t_qs + lane_addr + 32u * b, x);
+          tc_ld_32x32b_x32(t_pv + lane_addr + 32u * b, y);
+          tc_wait_ld();
+          if (b == 3) {
+            tc_fence_before();
+            arrive(sh.bars.drained);
+          }
+          uint32_t u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float o0 = fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa);
+            float o1 = fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa);
+            if (bad) {
+              if (ch * kC + i >= sh.bad_at[32 * b + 2 * j]) o0 = __int_as_float(0x7fffffff);
+              if (ch * kC + i >= sh.bad_at[32 * b + 2 * j + 1]) o1 = __int_as_float(0x7fffffff);
+            }
+            u[j] = pack2(o0, o1);
+          }
+          if (in) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              __half* p = row + 32 * b + 16 * j;
+              const uint32_t* z = u + 8 * j;
+              if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(z[0]),
+                             "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+                             : "memory");
+              } else {
+                *reinterpret_cast<uint4*>(p) = make_uint4(z[0], z[1], z[2], z[3]);
+                *reinterpret_cast<uint4*>(p + 8) = make_uint4(z[4], z[5], z[6], z[7]);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Every MMA has completed (the MMA warp drained them) and every TMEM read is done.
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+template <bool kState>
+cudaError_t launch(const LinCall& c, const LinMaps& maps, cudaStream_t s) {
+  using L = Lay<kState>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t attr[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    attr[dev] = cudaFuncSetAttribute(lin_tc_kernel<kState>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  });
+  if (attr[dev] != cudaSuccess) return attr[dev];
+  const dim3 grid(static_cast<unsigned>(c.n_items), static_cast<unsigned>(c.H),
+                  static_cast<unsigned>(c.n_sweeps));
+  lin_tc_kernel<kState><<<grid, kThreads, L::kSmem, s>>>(c, maps);
+  return cudaGetLastError();
+}
+
+// A matrix of heads as rows of tokens: head h begins at column h * head_stride of every row (the
+// rows may overlap in memory, which only loads ever see).
+bool map_heads(CUtensorMap* m, const void* p, int64_t T, int H, int64_t t_stride, int64_t h_stride) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p,
+                      static_cast<uint64_t>((H - 1) * h_stride + kD), static_cast<uint64_t>(T),
+                      static_cast<uint64_t>(t_stride) * 2, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+bool lin_tc_supported(const LinCall& c) {
+  if (c.dt != kInF16) return false;
+  for (int i = 0; i < c.n_sweeps; ++i) {
+    const LinSweep& w = c.sw[i];
+    if (w.dk != kD || w.dv != kD) return false;
+    const int64_t st[3][2] = {{w.q_t, w.q_h}, {w.k_t, w.k_h}, {w.v_t, w.v_h}};
+    for (const auto& x : st)
+      // a row that every token shares has no tensor map, and columns are counted in 31 bits
+      if (x[0] == 0 || x[0] >= (1ll << 38) || (c.H - 1) * x[1] + kD > 0x7fffffff) return false;
+  }
+  return true;
+}
+
+cudaError_t launch_lin_tc(const LinCall& c, cudaStream_t s) {
+  LinMaps maps;
+  for (int i = 0; i < c.n_sweeps; ++i) {
+    const LinSweep& w = c.sw[i];
+    if (!map_heads(&maps.m[3 * i], w.k, c.T, c.H, w.k_t, w.k_h) ||
+        !map_heads(&maps.m[3 * i + 1], w.v, c.T, c.H, w.v_t, w.v_h) ||
+        !map_heads(&maps.m[3 * i + 2], w.q, c.T, c.H, w.q_t, w.q_h))
+      return cudaErrorInvalidValue;
+  }
+  if (c.split) {
+    cudaError_t e = launch<true>(c, maps, s);
+    if (e == cudaSuccess) e = launch_lin_join(c, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch<false>(c, maps, s);
+}
+
+}  // namespace mmf

@@ -602,7 +602,7 @@ void lin_call(const mmf_linattn_desc* d, int n_sweeps, LinCall* c) {
   c->H = d->H;
   c->cu = d->cu_seqlens;
   c->log_decay = d->log_decay;
-  lin_plan(d->T, d->B, d->cu_seqlens != nullptr, d->H, d->dk, d->dv, n_sweeps, &c->seg_len,
+  lin_plan(d->T, d->B, d->cu_seqlens != nullptr, d->H, d->dk, d->dv, c->dt, n_sweeps, &c->seg_len,
            &c->n_items, &c->split);
 }
 
