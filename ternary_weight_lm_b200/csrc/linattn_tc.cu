@@ -12,8 +12,9 @@
 // All operands sit in shared memory as the 128-byte-swizzled tiles that TMA writes, so the same
 // image of K serves Q K^T (K-major) and V^T K' (MN-major), and V likewise.
 //
-// Warps: 0 TMA, 1 TMEM and MMA issue, 2-5 the state's (thread = column of v = row of S^T, whose 128
-// values stay in its registers; also K -> K'), 6-9 the rows' (thread = token: scores and outputs).
+// Warps: 0 TMA, 1 TMEM and MMA issue, 4-7 the state's (thread = column of v = row of S^T, whose 128
+// values stay in its registers; also K -> K'), 8-11 the rows' (thread = token: scores and outputs).
+// The first four warps give registers to the other eight.
 // Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' is carried as two
 // fp16 parts (22 bits), since the state is an fp32 output: the first overwrites K once Q K^T is
 // done, the second overwrites Q once Q S is done as well.  TMEM: P, Q S, P V, V^T K', 128 columns
@@ -48,7 +49,8 @@ constexpr int kD = 128;                      // head size, k and v
 constexpr int kC = 128;                      // tokens of a chunk
 constexpr int kPanel = kC * 128;             // 128 rows x 64 fp16
 constexpr int kTile = 2 * kPanel;            // 32 KB
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+constexpr int kRegsFew = 56, kRegsMany = 224;   // 56 + 2 * 224 = 3 * 168, what the block is launched with
 constexpr int kGroup = 128;                  // threads of the state warps, and of the row warps
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -134,14 +136,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-// Exponent of the power of two that brings a magnitude (as bits) to 2^14 .. 2^15; zeros take none.
-__device__ __forceinline__ int up_to_half(uint32_t bits) {
-  return bits == 0u ? 0 : max(-100, min(14 + 127 - static_cast<int>(bits >> 23), 100));
+// Exponent of the power of two that brings a magnitude to 2^14 .. 2^15; zeros take none.
+__device__ __forceinline__ int up_to_half(float top) {
+  return top == 0.0f ? 0 : max(-100, min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 100));
+}
+__device__ __forceinline__ float warp_max(float magnitude) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(magnitude)));
+}
+__device__ __forceinline__ float max4(const float (&x)[4]) {
+  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -161,6 +165,25 @@ struct LinMaps {
   CUtensorMap m[3 * kMaxSweeps];
 };
 
+// A bounded wait that looks at the clock only once in many tries: the roles hand over to one
+// another several times a chunk, and a read of the global timer in that path costs microseconds.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             unsigned* status) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
 struct Bars {
   uint64_t full[2], empty[2];
   uint64_t scores, qk, p, v, k, out, drained, upd, state, drain;
@@ -168,8 +191,10 @@ struct Bars {
 
 struct Shared {
   Bars bars;
-  float pow[kC + 1];        // gamma^0 .. gamma^128
-  uint32_t red_k[4], red_s[4];
+  float zeros[32];          // pow[-32] .. pow[-1]: the factor of a later token's score
+  float pow[kC + 4];        // gamma^0 .. gamma^128
+  float col[32];            // gamma^(31-j) forwards, gamma^j backwards
+  float red_k[4], red_w[4], red_s[4];
   int exp_s[2];             // exponent of the fp16 state, by chunk parity
   int exp_k[2];             // of K'
   int bad_at[kD];           // first position of the segment whose v is not finite, by column
@@ -228,6 +253,10 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (!kState) tma_prefetch_desc(mq);
   }
   if (tid <= kC) sh.pow[tid] = lin_power(lin_lg2(c, h), tid);
+  if (tid < 32) {
+    sh.zeros[tid] = 0.0f;
+    sh.col[tid] = lin_power(lin_lg2(c, h), back ? tid : 31 - tid);
+  }
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), L::kCols);
@@ -241,8 +270,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   volatile int* abort_flag = &sh.abort;
   // waits of a whole warp, with one outcome
   auto wait = [&](uint64_t& bar, int parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), static_cast<uint32_t>(parity),
-                                                     kWaitLimitNs, abort_flag, c.status));
+    return __all_sync(0xffffffffu, wait_bounded(smem_u32(&bar), static_cast<uint32_t>(parity),
+                                                abort_flag, c.status));
   };
   auto arrive = [&](uint64_t& bar) {   // once for the warp, after all its lanes
     __syncwarp();
@@ -265,14 +294,19 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
       for (int x = 0; x < 16; ++x) sts128(vec_at(t, r, x), make_uint4(0u, 0u, 0u, 0u));
     } else {
-      uint32_t odd = 0u;   // an exponent of all ones carries into its sign's place
+      // 0 times what is not finite is NaN
+      __half2 odd[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd[e] = __float2half2_rn(0.0f);
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const uint4 v = lds128(vec_at(t, r, x));
-        odd |= ((v.x & 0x7c007c00u) + 0x04000400u) | ((v.y & 0x7c007c00u) + 0x04000400u) |
-               ((v.z & 0x7c007c00u) + 0x04000400u) | ((v.w & 0x7c007c00u) + 0x04000400u);
+        const __half2* hv = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd[e] = __hfma2(hv[e], __float2half2_rn(0.0f), odd[e]);
       }
-      if (odd & 0x80008000u) {
+      const float2 sum = __half22float2(__hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3])));
+      if (!(sum.x + sum.y == 0.0f)) {
         for (int col = 0; col < kD; ++col) {
           const uint32_t a = vec_at(t, r, col >> 3) + 2u * (col & 7);
           uint16_t x;
@@ -288,46 +322,54 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     fence_proxy_async_smem();
   };
   // Row r of K' from row r of K: a gamma^(tokens after it) k_j in two fp16 parts, scaled by the
-  // chunk's power of two.  False if one of the group's warps gave up (`ok`).
+  // chunk's power of two.  With the factor w 2^e = wh + wl in fp16, hi = k wh rounded, and the rest
+  // (k wh - hi, exact, plus k wl) is lo: three half2 operations, an error of about 2^-22.  e brings
+  // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
+  // that is less.  False if one of the group's warps gave up (`ok`).
   auto decay_k = [&](int chunk, int r, int id, bool ok) {
     const int s = chunk & 1, n = tokens(chunk), pos = back ? kC - 1 - r : r;
     const uint32_t t = tile_k(s), t2 = tile_q(s);
     const bool in = pos < n;
     const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
-    __half2 m2 = __float2half2_rn(0.0f);
-    if (ok) {
+    float top = 0.0f;
+    if (ok && in) {
+      __half2 m[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.0f);
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const uint4 v = lds128(vec_at(t, r, x));
         const __half2* hv = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m2 = __hmax2(m2, __habs2(hv[e]));
+        for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(hv[e]));
       }
+      const float2 y = __half22float2(__hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3])));
+      top = fmaxf(y.x, y.y);
     }
-    uint32_t top = 0u;
-    if (in) top = max(magnitude(__low2float(m2) * wt), magnitude(__high2float(m2) * wt));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) sh.red_k[r >> 5] = top;
+    const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
+    top = warp_max(top * fabsf(wt));
+    if (lane == 0) {
+      sh.red_k[r >> 5] = top;
+      sh.red_w[r >> 5] = wide;
+    }
     if (!named_bar_and(id, kGroup, ok)) return false;
-    const int e = up_to_half(max(max(sh.red_k[0], sh.red_k[1]), max(sh.red_k[2], sh.red_k[3])));
+    const int e = min(up_to_half(max4(sh.red_k)), up_to_half(max4(sh.red_w)));
     if (r == 0) sh.exp_k[s] = e;
     const float f = wt * pow2(e);
-#pragma unroll 4
+    const __half fh = __float2half_rn(f);
+    const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
+#pragma unroll
     for (int x = 0; x < 16; ++x) {
       uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
       if (in) {
         const uint4 v = lds128(vec_at(t, r, x));
-        const uint32_t* vi = reinterpret_cast<const uint32_t*>(&v);
-        uint32_t* ho = reinterpret_cast<uint32_t*>(&hi);
-        uint32_t* lo_ = reinterpret_cast<uint32_t*>(&lo);
+        const __half2* k2 = reinterpret_cast<const __half2*>(&v);
+        __half2* h2 = reinterpret_cast<__half2*>(&hi);
+        __half2* l2 = reinterpret_cast<__half2*>(&lo);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 y = unpack2(vi[i]);
-          y.x *= f;
-          y.y *= f;
-          ho[i] = pack2(y.x, y.y);
-          const float2 z = unpack2(ho[i]);
-          lo_[i] = pack2(y.x - z.x, y.y - z.y);
+          h2[i] = __hmul2(k2[i], wh);
+          l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
         }
       }
       sts128(vec_at(t, r, x), hi);
@@ -337,16 +379,17 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     return true;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------------------ TMA
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------------------------- TMA
       const uint64_t pol = l2_policy_evict_normal();
       auto col = [&](int64_t stride) { return static_cast<int32_t>(h * stride); };
       int issued = 0;
       for (int ch = 0; ch < chunks; ++ch) {
         const int s = ch & 1;
-        if (ch >= 2 && !mbar_wait_bounded(smem_u32(&sh.bars.empty[s]), ((ch >> 1) - 1) & 1,
-                                          kWaitLimitNs, abort_flag, c.status))
+        if (ch >= 2 && !wait_bounded(smem_u32(&sh.bars.empty[s]), ((ch >> 1) - 1) & 1, abort_flag,
+                                     c.status))
           break;
         const uint32_t bar = smem_u32(&sh.bars.full[s]);
         mbar_arrive_expect_tx(bar, (kState ? 2 : 3) * kTile);
@@ -362,7 +405,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       for (int ch = issued > 2 ? issued - 2 : 0; ch < issued; ++ch)   // all land before the block ends
         mbar_wait_bounded(smem_u32(&sh.bars.full[ch & 1]), (ch >> 1) & 1, kDrainNs, nullptr, c.status);
     }
-  } else if (warp == 1) {
+    if (warp == 1) {
     // ------------------------------------------------------------------------------ MMA
     auto commit = [&](uint64_t& bar) { tc_commit_warp(smem_u32(&bar)); };
     if constexpr (kState) {
@@ -410,8 +453,10 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     commit(sh.bars.drain);
     mbar_wait_bounded(smem_u32(&sh.bars.drain), 0, kDrainNs, nullptr, c.status);
     __syncwarp();
-  } else if (warp < 6) {
+    }
+  } else if (warp < 8) {
     // ------------------------------------------------------------------------------ state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: row of S^T
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
     const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * kD * kD;
@@ -430,17 +475,17 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
       for (int i = 0; i < kD; ++i) S[i] = from ? from[i * sk + r * sv] : 0.0f;
     }
-    uint32_t top = 0u;
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (!kState) {
 #pragma unroll
-      for (int i = 0; i < kD; ++i) top = max(top, magnitude(S[i]));
+      for (int i = 0; i < kD; ++i) top[i & 3] = fmaxf(top[i & 3], fabsf(S[i]));
     }
     // the state for chunk ch: scaled, rounded and written as the B operand of Q S
     auto publish = [&](int ch, bool ok) {
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) sh.red_s[q] = top;
+      const float m = warp_max(max4(top));
+      if (lane == 0) sh.red_s[q] = m;
       if (!named_bar_and(1, kGroup, ok)) return false;
-      const int e = up_to_half(max(max(sh.red_s[0], sh.red_s[1]), max(sh.red_s[2], sh.red_s[3])));
+      const int e = up_to_half(max4(sh.red_s));
       if (r == 0) sh.exp_s[ch & 1] = e;
       const float f = pow2(e);
 #pragma unroll
@@ -473,7 +518,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       if (w2) {
         tc_fence_after();
         const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[s]);
-        top = 0u;
+        top[0] = top[1] = top[2] = top[3] = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           uint32_t d[32];
@@ -483,7 +528,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
           for (int i = 0; i < 32; ++i) {
             float& x = S[32 * b + i];
             x = fmaf(decay, x, __uint_as_float(d[i]) * f);
-            if constexpr (!kState) top = max(top, magnitude(x));
+            if constexpr (!kState) top[i & 3] = fmaxf(top[i & 3], fabsf(x));
           }
         }
         tc_fence_before();
@@ -507,6 +552,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     }
   } else {
     // ------------------------------------------------------------------------------- rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: token row
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
     if constexpr (kState) {
@@ -525,44 +571,64 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         tc_fence_after();
         int e;
         {
-          float P[kC];
-          uint32_t top = 0u;
+          // gamma^(i-j): of a block of 32 columns before the warp's rows, a row's factor times a
+          // column's, both at most 1; of the block across them, from the table
+          float P[kC], rowf[4], top[4];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            // blocks of 32 columns: before the warp's rows, across them, after them
-            const bool past = back ? b > q : b < q;
-            if (past || b == q) {
+            top[b] = rowf[b] = 0.0f;
+            if (b == q) {
               uint32_t d[32];
               tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
               tc_wait_ld();
-              // gamma^(i-j) of a whole block: a row's factor times a column's, both at most 1
-              const float rowf = past ? w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31] : w.a;
+              rowf[b] = w.a;
+              const float* pw = back ? sh.pow - lane : sh.pow + lane;
+              // not a product with 0: the score of a later token may be anything
+              const uint32_t earlier = back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+              if (back) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                float f;
-                if (past) {
-                  f = rowf * sh.pow[back ? j : 31 - j];
-                } else {
-                  const int d1 = back ? j - lane : lane - j;
-                  f = d1 >= 0 ? rowf * sh.pow[d1] : 0.0f;
-                }
-                // not a product with 0: the score of a later token may be anything
-                const float x = (past || (back ? j >= lane : j <= lane)) ? __uint_as_float(d[j]) * f : 0.0f;
-                P[32 * b + j] = x;
-                top = max(top, magnitude(x));
+                for (int j = 0; j < 32; ++j)
+                  P[32 * b + j] = (earlier >> j) & 1u ? __uint_as_float(d[j]) * pw[j] : 0.0f;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  P[32 * b + j] = (earlier >> j) & 1u ? __uint_as_float(d[j]) * pw[-j] : 0.0f;
+              }
+            } else if (back ? b > q : b < q) {
+              uint32_t d[32];
+              tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
+              tc_wait_ld();
+              rowf[b] = w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31];
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&sh.col[j]);
+                P[32 * b + j] = __uint_as_float(d[j]) * f.x;
+                P[32 * b + j + 1] = __uint_as_float(d[j + 1]) * f.y;
+                P[32 * b + j + 2] = __uint_as_float(d[j + 2]) * f.z;
+                P[32 * b + j + 3] = __uint_as_float(d[j + 3]) * f.w;
               }
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) P[32 * b + j] = 0.0f;
             }
           }
-          e = up_to_half(top);
-          const float f = pow2(e);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top[b] = fmaxf(top[b], fabsf(P[32 * b + j]));
+            top[b] *= fabsf(rowf[b]);
+          }
+          e = up_to_half(max4(top));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) rowf[b] *= pow2(e);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint32_t u[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) u[j] = pack2(P[64 * b + 2 * j] * f, P[64 * b + 2 * j + 1] * f);
+            for (int j = 0; j < 32; ++j) {
+              const float f = rowf[2 * b + (j >> 4)];
+              u[j] = pack2(P[64 * b + 2 * j] * f, P[64 * b + 2 * j + 1] * f);
+            }
             tc_st_32x32b_x32(t_p + lane_addr + 32u * b, u);
           }
           tc_wait_st();
@@ -580,7 +646,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         __half* row = op + (row0(ch) + r) * w.o_t;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          uint32_t x[32], y[32];
+          uint32_t x[32], y[32], bad_cols = 0u;
           tc_ld_32x32b_x32(t_qs + lane_addr + 32u * b, x);
           tc_ld_32x32b_x32(t_pv + lane_addr + 32u * b, y);
           tc_wait_ld();
@@ -588,16 +654,23 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
             tc_fence_before();
             arrive(sh.bars.drained);
           }
+          if (bad) {
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+              if (ch * kC + i >= sh.bad_at[32 * b + j]) bad_cols |= 1u << j;
+          }
           uint32_t u[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float o0 = fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa);
-            float o1 = fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa);
-            if (bad) {
-              if (ch * kC + i >= sh.bad_at[32 * b + 2 * j]) o0 = __int_as_float(0x7fffffff);
-              if (ch * kC + i >= sh.bad_at[32 * b + 2 * j + 1]) o1 = __int_as_float(0x7fffffff);
-            }
+            const float o0 = fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa);
+            const float o1 = fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa);
             u[j] = pack2(o0, o1);
+          }
+          if (bad_cols) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              u[j] |= ((bad_cols >> (2 * j)) & 1u ? 0x7fffu : 0u) |
+                      ((bad_cols >> (2 * j + 1)) & 1u ? 0x7fff0000u : 0u);
           }
           if (in) {
 #pragma unroll
