@@ -132,6 +132,15 @@ __device__ __forceinline__ void product_tm(uint32_t d, uint32_t a, uint32_t b) {
     mma_ts(d, a + 8u * k, bd + static_cast<uint64_t>((k * 16 * 128) >> 4), idesc, k > 0 ? 1u : 0u);
 }
 
+__device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -291,14 +300,14 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int s = chunk & 1, pos = back ? kC - 1 - r : r;
     const uint32_t t = tile_v(s);
     if (pos >= tokens(chunk)) {
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < 16; ++x) sts128(vec_at(t, r, x), make_uint4(0u, 0u, 0u, 0u));
     } else {
       // 0 times what is not finite is NaN
       __half2 odd[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) odd[e] = __float2half2_rn(0.0f);
-#pragma unroll
+#pragma unroll 8
       for (int x = 0; x < 16; ++x) {
         const uint4 v = lds128(vec_at(t, r, x));
         const __half2* hv = reinterpret_cast<const __half2*>(&v);
@@ -307,6 +316,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       }
       const float2 sum = __half22float2(__hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3])));
       if (!(sum.x + sum.y == 0.0f)) {
+#pragma unroll 1
         for (int col = 0; col < kD; ++col) {
           const uint32_t a = vec_at(t, r, col >> 3) + 2u * (col & 7);
           uint16_t x;
@@ -336,7 +346,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       __half2 m[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.0f);
-#pragma unroll
+#pragma unroll 8
       for (int x = 0; x < 16; ++x) {
         const uint4 v = lds128(vec_at(t, r, x));
         const __half2* hv = reinterpret_cast<const __half2*>(&v);
@@ -358,7 +368,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float f = wt * pow2(e);
     const __half fh = __float2half_rn(f);
     const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
-#pragma unroll
+#pragma unroll 4
     for (int x = 0; x < 16; ++x) {
       uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
       if (in) {
@@ -571,65 +581,63 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         tc_fence_after();
         int e;
         {
-          // gamma^(i-j): of a block of 32 columns before the warp's rows, a row's factor times a
-          // column's, both at most 1; of the block across them, from the table
-          float P[kC], rowf[4], top[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            top[b] = rowf[b] = 0.0f;
-            if (b == q) {
-              uint32_t d[32];
-              tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
-              tc_wait_ld();
-              rowf[b] = w.a;
-              const float* pw = back ? sh.pow - lane : sh.pow + lane;
-              // not a product with 0: the score of a later token may be anything
-              const uint32_t earlier = back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-              if (back) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  P[32 * b + j] = (earlier >> j) & 1u ? __uint_as_float(d[j]) * pw[j] : 0.0f;
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  P[32 * b + j] = (earlier >> j) & 1u ? __uint_as_float(d[j]) * pw[-j] : 0.0f;
-              }
-            } else if (back ? b > q : b < q) {
-              uint32_t d[32];
-              tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
-              tc_wait_ld();
-              rowf[b] = w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31];
+          // gamma^(i-j) q_i . k_j of a block of 32 columns, without the row's factor.  Before the
+          // warp's rows it is that factor times a column's, both at most 1; across them, from the
+          // table.  Not a product with 0: the score of a later token may be anything.
+          auto scores = [&](int b, float (&x)[32]) {
+            uint32_t d[32];
+            tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
+            tc_wait_ld();
+            if (b != q) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&sh.col[j]);
-                P[32 * b + j] = __uint_as_float(d[j]) * f.x;
-                P[32 * b + j + 1] = __uint_as_float(d[j + 1]) * f.y;
-                P[32 * b + j + 2] = __uint_as_float(d[j + 2]) * f.z;
-                P[32 * b + j + 3] = __uint_as_float(d[j + 3]) * f.w;
+                x[j] = __uint_as_float(d[j]) * f.x;
+                x[j + 1] = __uint_as_float(d[j + 1]) * f.y;
+                x[j + 2] = __uint_as_float(d[j + 2]) * f.z;
+                x[j + 3] = __uint_as_float(d[j + 3]) * f.w;
               }
+            } else if (back) {
+              const float* pw = sh.pow - lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = j >= lane ? __uint_as_float(d[j]) * pw[j] : 0.0f;
+            } else {
+              const float* pw = sh.pow + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = j <= lane ? __uint_as_float(d[j]) * pw[-j] : 0.0f;
+            }
+          };
+          auto row_factor = [&](int b) {
+            return b == q ? w.a : w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31];
+          };
+          // two passes over TMEM, so that a block's values need not stay (and the loops need not be
+          // unrolled: their code would not fit the instruction cache beside the other roles')
+          const int b0 = back ? q : 0, b1 = back ? 3 : q;
+          float most = 0.0f;
+#pragma unroll 1
+          for (int b = b0; b <= b1; ++b) {
+            float x[32], top[4] = {0.f, 0.f, 0.f, 0.f};
+            scores(b, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(x[j]));
+            most = fmaxf(most, max4(top) * fabsf(row_factor(b)));
+          }
+          e = up_to_half(most);
+          // ascending blocks: the packed columns of a block lie on blocks that are done with
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t u[16];
+            if (b >= b0 && b <= b1) {
+              float x[32];
+              scores(b, x);
+              const float f = row_factor(b) * pow2(e);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] = pack2(x[2 * j] * f, x[2 * j + 1] * f);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) P[32 * b + j] = 0.0f;
+              for (int j = 0; j < 16; ++j) u[j] = 0u;
             }
-          }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) top[b] = fmaxf(top[b], fabsf(P[32 * b + j]));
-            top[b] *= fabsf(rowf[b]);
-          }
-          e = up_to_half(max4(top));
-#pragma unroll
-          for (int b = 0; b < 4; ++b) rowf[b] *= pow2(e);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint32_t u[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float f = rowf[2 * b + (j >> 4)];
-              u[j] = pack2(P[64 * b + 2 * j] * f, P[64 * b + 2 * j + 1] * f);
-            }
-            tc_st_32x32b_x32(t_p + lane_addr + 32u * b, u);
+            st_x16(t_p + lane_addr + 16u * b, u);
           }
           tc_wait_st();
           tc_fence_before();
@@ -644,7 +652,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         const bool in = i < tokens(ch);
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         __half* row = op + (row0(ch) + r) * w.o_t;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           uint32_t x[32], y[32], bad_cols = 0u;
           tc_ld_32x32b_x32(t_qs + lane_addr + 32u * b, x);
