@@ -12,13 +12,15 @@
 // All operands sit in shared memory as the 128-byte-swizzled tiles that TMA writes, so the same
 // image of K serves Q K^T (K-major) and V^T K' (MN-major), and V likewise.
 //
-// Warps: 0 TMA, 1 TMEM and MMA issue, 4-7 the state's (thread = column of v = row of S^T, whose 128
-// values stay in its registers; also K -> K'), 8-11 the rows' (thread = token: scores and outputs).
-// The first four warps give registers to the other eight.
-// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' is carried as two
-// fp16 parts (22 bits), since the state is an fp32 output: the first overwrites K once Q K^T is
-// done, the second overwrites Q once Q S is done as well.  TMEM: P, Q S, P V, V^T K', 128 columns
-// each; the fp16 P overwrites P.
+// Warps: 0 TMA, 1 TMEM and MMA issue; then groups of four, a thread for each row of their tile:
+// 4-7 the state's (row = column of v; its 128 values stay in the thread's registers), 8-11 K -> K',
+// 12-15 and 16-19 the tokens' (scores and outputs), taking turns at the chunks, so that one's
+// outputs overlap the other's scores.  Registers go from the first group to the state's.
+// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' overwrites K once
+// Q K^T is done.  Where the state is an output (fp32), K' has a second fp16 part (22 bits in all),
+// which overwrites Q once Q S is done.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P
+// overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
+// stay in the instruction cache.
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
 // K' scaled by powers of two (a row's, the state's, the chunk's) before they are rounded.  The
@@ -28,8 +30,8 @@
 // are replaced by zero on arrival and their place is noted: from that token on the column's
 // outputs and state are NaN.
 //
-// kState: the state alone (pass one of a split sequence).  There the row warps turn K into K'
-// while the state warps add the chunk before.
+// kState: the state alone (pass one of a split sequence).  There the tokens' two groups turn K into
+// K', in turns, and the group for it idles.
 //
 // Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
 // copies and MMAs in flight are drained and TMEM is freed.
@@ -49,8 +51,10 @@ constexpr int kD = 128;                      // head size, k and v
 constexpr int kC = 128;                      // tokens of a chunk
 constexpr int kPanel = kC * 128;             // 128 rows x 64 fp16
 constexpr int kTile = 2 * kPanel;            // 32 KB
-constexpr int kThreads = 384;
-constexpr int kRegsFew = 56, kRegsMany = 224;   // 56 + 2 * 224 = 3 * 168, what the block is launched with
+constexpr int kThreads = 640;
+// Registers of the groups' threads; together 5 * 96, what the block is launched with.
+constexpr int kRegsIssue = 40, kRegsState = 184, kRegsDecay = 64, kRegsRows = 96;
+static_assert(kRegsIssue + kRegsState + kRegsDecay + 2 * kRegsRows <= 5 * 96, "registers");
 constexpr int kGroup = 128;                  // threads of the state warps, and of the row warps
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -193,19 +197,25 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// A wait names a phase by its parity, so whoever waits must come before the phase after the next
+// has completed, and not before the phase before has.  Barriers with two places (the even and the
+// odd chunks') are handed over by groups that can run a chunk ahead of the waiting one, or are
+// waited for every other chunk; stages are reused only after every hand-over of their chunk, which
+// keeps either from getting two chunks ahead.
 struct Bars {
   uint64_t full[2], empty[2];
-  uint64_t scores, qk, p, v, k, out, drained, upd, state, drain;
+  uint64_t scores[2], p[2], out[2], drained[2], k[2], v[2], state[2];
+  uint64_t qk, upd, drain;
 };
 
 struct Shared {
   Bars bars;
   float zeros[32];          // pow[-32] .. pow[-1]: the factor of a later token's score
   float pow[kC + 4];        // gamma^0 .. gamma^128
-  float col[32];            // gamma^(31-j) forwards, gamma^j backwards
-  float red_k[4], red_w[4], red_s[4];
-  int exp_s[2];             // exponent of the fp16 state, by chunk parity
-  int exp_k[2];             // of K'
+  alignas(16) float col[32];   // gamma^(31-j) forwards, gamma^j backwards
+  float red_k[2][4], red_w[2][4], red_s[4];
+  int exp_s[2];             // exponent of the fp16 state, by chunk
+  int exp_k[4];             // of K'
   int bad_at[kD];           // first position of the segment whose v is not finite, by column
   int any_bad;
   uint32_t tmem;
@@ -243,16 +253,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.bars.full[s]), 1);
       mbar_init(smem_u32(&sh.bars.empty[s]), 1);
+      mbar_init(smem_u32(&sh.bars.scores[s]), 1);
+      mbar_init(smem_u32(&sh.bars.p[s]), 4);
+      mbar_init(smem_u32(&sh.bars.out[s]), 1);
+      mbar_init(smem_u32(&sh.bars.drained[s]), 4);
+      mbar_init(smem_u32(&sh.bars.k[s]), 4);
+      mbar_init(smem_u32(&sh.bars.v[s]), 4);
+      mbar_init(smem_u32(&sh.bars.state[s]), 4);
     }
-    mbar_init(smem_u32(&sh.bars.scores), 1);
     mbar_init(smem_u32(&sh.bars.qk), 1);
-    mbar_init(smem_u32(&sh.bars.p), 4);
-    mbar_init(smem_u32(&sh.bars.v), 4);
-    mbar_init(smem_u32(&sh.bars.k), 4);
-    mbar_init(smem_u32(&sh.bars.out), 1);
-    mbar_init(smem_u32(&sh.bars.drained), 4);
     mbar_init(smem_u32(&sh.bars.upd), 1);
-    mbar_init(smem_u32(&sh.bars.state), 4);
     mbar_init(smem_u32(&sh.bars.drain), 1);
     sh.abort = 0;
     sh.any_bad = 0;
@@ -336,9 +346,11 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   // (k wh - hi, exact, plus k wl) is lo: three half2 operations, an error of about 2^-22.  e brings
   // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
   // that is less.  False if one of the group's warps gave up (`ok`).
-  auto decay_k = [&](int chunk, int r, int id, bool ok) {
-    const int s = chunk & 1, n = tokens(chunk), pos = back ? kC - 1 - r : r;
-    const uint32_t t = tile_k(s), t2 = tile_q(s);
+  // find_exp: e and the row's factor; false if one of the group's warps gave up (`ok`).
+  auto find_exp = [&](int chunk, int r, int id, bool ok, float* f) {
+    const int set = chunk & 1;   // written again only after the whole group handed the chunk over
+    const int n = tokens(chunk), pos = back ? kC - 1 - r : r;
+    const uint32_t t = tile_k(chunk & 1);
     const bool in = pos < n;
     const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
     float top = 0.0f;
@@ -359,38 +371,48 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
     top = warp_max(top * fabsf(wt));
     if (lane == 0) {
-      sh.red_k[r >> 5] = top;
-      sh.red_w[r >> 5] = wide;
+      sh.red_k[set][r >> 5] = top;
+      sh.red_w[set][r >> 5] = wide;
     }
     if (!named_bar_and(id, kGroup, ok)) return false;
-    const int e = min(up_to_half(max4(sh.red_k)), up_to_half(max4(sh.red_w)));
-    if (r == 0) sh.exp_k[s] = e;
-    const float f = wt * pow2(e);
+    const int e = min(up_to_half(max4(sh.red_k[set])), up_to_half(max4(sh.red_w[set])));
+    if (r == 0) sh.exp_k[chunk & 3] = e;
+    *f = wt * pow2(e);
+    return true;
+  };
+  auto decay_k = [&](int chunk, int r, float f, bool two) {
+    const uint32_t t = tile_k(chunk & 1), t2 = tile_q(chunk & 1);
+    const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
     const __half fh = __float2half_rn(f);
     const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
-#pragma unroll 4
-    for (int x = 0; x < 16; ++x) {
-      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-      if (in) {
-        const uint4 v = lds128(vec_at(t, r, x));
-        const __half2* k2 = reinterpret_cast<const __half2*>(&v);
+#pragma unroll 1
+    for (int x0 = 0; x0 < 16; x0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = in ? lds128(vec_at(t, r, x0 + x)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint4 hi, lo;
+        const __half2* k2 = reinterpret_cast<const __half2*>(&v[x]);
         __half2* h2 = reinterpret_cast<__half2*>(&hi);
         __half2* l2 = reinterpret_cast<__half2*>(&lo);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h2[i] = __hmul2(k2[i], wh);
-          l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
+        for (int i = 0; i < 4; ++i) h2[i] = __hmul2(k2[i], wh);
+        sts128(vec_at(t, r, x0 + x), hi);
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
+          sts128(vec_at(t2, r, x0 + x), lo);
         }
       }
-      sts128(vec_at(t, r, x), hi);
-      sts128(vec_at(t2, r, x), lo);
     }
     fence_proxy_async_smem();
-    return true;
   };
+  // the state is an output: K' in two parts
+  const bool two = kState || (whole && w.sT != nullptr);
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------------------------- TMA
       const uint64_t pol = l2_policy_evict_normal();
@@ -418,47 +440,44 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (warp == 1) {
     // ------------------------------------------------------------------------------ MMA
     auto commit = [&](uint64_t& bar) { tc_commit_warp(smem_u32(&bar)); };
-    if constexpr (kState) {
-      for (int ch = 0; ch < chunks; ++ch) {
-        const int s = ch & 1;
+    bool ok = true;
+    for (int ch = 0; ok && ch < chunks; ++ch) {
+      const int s = ch & 1, ph = (ch >> 1) & 1;
+      if constexpr (kState) {
         // K' and V are ready, and the update before is read
-        if (!wait(sh.bars.k, ch & 1)) break;
-        if (ch > 0 && !wait(sh.bars.state, (ch - 1) & 1)) break;
+        ok = wait(sh.bars.k[s], ph) && (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
+        if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), false);
         product_mn(t_upd, tile_v(s), tile_q(s), true);
         commit(sh.bars.upd);
-        commit(sh.bars.empty[s]);
-      }
-    } else {
-      bool ok = true;
-      for (int ch = 0; ok && ch < chunks; ++ch) {
-        const int s = ch & 1;
+      } else {
         // scores, in P's place: the product that read it last has completed
-        ok = wait(sh.bars.full[s], (ch >> 1) & 1) && (ch == 0 || wait(sh.bars.out, (ch - 1) & 1));
+        ok = wait(sh.bars.full[s], ph) && (ch == 0 || wait(sh.bars.out[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         product_kk(t_p, tile_q(s), tile_k(s));
-        commit(sh.bars.scores);
+        commit(sh.bars.scores[s]);
         // Q S: the state is in shared memory, and the outputs before are read
-        ok = wait(sh.bars.state, ch & 1) && (ch == 0 || wait(sh.bars.drained, (ch - 1) & 1));
+        ok = wait(sh.bars.state[s], ph) &&
+             (ch == 0 || wait(sh.bars.drained[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         product_kk(t_qs, tile_q(s), tile_s);
         commit(sh.bars.qk);
-        ok = wait(sh.bars.v, ch & 1) && wait(sh.bars.p, ch & 1);
-        if (!ok) break;
-        tc_fence_after();
-        product_tm(t_pv, t_p, tile_v(s));
-        commit(sh.bars.out);
-        ok = wait(sh.bars.k, ch & 1);
+        ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph);
         if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), false);
-        product_mn(t_upd, tile_v(s), tile_q(s), true);
+        if (two) product_mn(t_upd, tile_v(s), tile_q(s), true);
         commit(sh.bars.upd);
-        commit(sh.bars.empty[s]);
+        ok = wait(sh.bars.p[s], ph);
+        if (!ok) break;
+        tc_fence_after();
+        product_tm(t_pv, t_p, tile_v(s));
+        commit(sh.bars.out[s]);
       }
+      commit(sh.bars.empty[s]);
     }
     commit(sh.bars.drain);
     mbar_wait_bounded(smem_u32(&sh.bars.drain), 0, kDrainNs, nullptr, c.status);
@@ -466,7 +485,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------------------ state
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
     const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: row of S^T
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
     const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * kD * kD;
@@ -504,30 +523,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
                make_uint4(pack2(S[8 * x] * f, S[8 * x + 1] * f), pack2(S[8 * x + 2] * f, S[8 * x + 3] * f),
                           pack2(S[8 * x + 4] * f, S[8 * x + 5] * f), pack2(S[8 * x + 6] * f, S[8 * x + 7] * f)));
       fence_proxy_async_smem();
-      arrive(sh.bars.state);
+      arrive(sh.bars.state[ch & 1]);
       return true;
     };
     bool ok = true;
     if constexpr (!kState) ok = publish(0, true);
     for (int ch = 0; ok && ch < chunks; ++ch) {
-      const int s = ch & 1;
-      if constexpr (!kState) {
-        bool w1 = wait(sh.bars.full[s], (ch >> 1) & 1);
-        if (w1) {
-          clean_v(ch, r);
-          arrive(sh.bars.v);
-        }
-        w1 = w1 && wait(sh.bars.qk, ch & 1);   // K and Q are no longer read as such
-        if (!decay_k(ch, r, 1, w1)) {
-          ok = false;
-          break;
-        }
-        arrive(sh.bars.k);
-      }
       const bool w2 = wait(sh.bars.upd, ch & 1);
       if (w2) {
         tc_fence_after();
-        const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[s]);
+        const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[ch & 3]);
         top[0] = top[1] = top[2] = top[3] = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -545,7 +550,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       }
       if constexpr (kState) {
         ok = w2;
-        if (ok) arrive(sh.bars.state);
+        if (ok) arrive(sh.bars.state[ch & 1]);
       } else {
         ok = publish(ch + 1, w2);
       }
@@ -560,92 +565,112 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
       for (int i = 0; i < kD; ++i) to[i * sk + r * sv] = bad ? __int_as_float(0x7fffffff) : S[i];
     }
-  } else {
-    // ------------------------------------------------------------------------------- rows
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
-    const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: token row
-    const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
-    if constexpr (kState) {
+  } else if (warp < 12) {
+    // --------------------------------------------------------------------------- K to K'
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecay));
+    if constexpr (!kState) {
+      const int r = 32 * (warp & 3) + lane;
       for (int ch = 0; ch < chunks; ++ch) {
-        const bool ok = wait(sh.bars.full[ch & 1], (ch >> 1) & 1);
+        const int s = ch & 1, ph = (ch >> 1) & 1;
+        bool ok = wait(sh.bars.full[s], ph);
+        if (ok) {
+          clean_v(ch, r);
+          arrive(sh.bars.v[s]);
+        }
+        float f;
+        if (!find_exp(ch, r, 2, ok, &f)) break;
+        // K, and with two parts Q, are no longer read as such
+        ok = two ? wait(sh.bars.qk, ch & 1) : wait(sh.bars.scores[s], ph);
+        if (!ok) break;
+        decay_k(ch, r, f, two);
+        arrive(sh.bars.k[s]);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------------------- tokens
+    const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: token row
+    const int turn = warp < 16 ? 0 : 1;
+    if constexpr (kState) {
+      for (int ch = turn; ch < chunks; ch += 2) {
+        const int ph = (ch >> 1) & 1;
+        const bool ok = wait(sh.bars.full[turn], ph);
+        float f;
         if (ok) clean_v(ch, r);
-        if (!decay_k(ch, r, 2, ok)) break;
-        arrive(sh.bars.k);
+        if (!find_exp(ch, r, 3 + turn, ok, &f)) break;
+        decay_k(ch, r, f, true);
+        arrive(sh.bars.k[turn]);
       }
     } else {
+      const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
       const int i = back ? kC - 1 - r : r;         // place in the chunk
       __half* op = static_cast<__half*>(w.o) + h * w.o_h;
       const bool wide = ((reinterpret_cast<uintptr_t>(op) | static_cast<uintptr_t>(2 * w.o_t)) & 31) == 0;
-      for (int ch = 0; ch < chunks; ++ch) {
-        if (!wait(sh.bars.scores, ch & 1)) break;
+      // blocks of 32 columns with tokens up to the warp's rows
+      const int b0 = back ? q : 0, b1 = back ? 3 : q;
+      // gamma^(i-j) a of a block but for the column's part: before the warp's rows a row's factor
+      // times a column's, both at most 1; across them, from the table
+      auto row_factor = [&](int b) {
+        return b == q ? w.a : w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31];
+      };
+      for (int ch = turn; ch < chunks; ch += 2) {
+        const int ph = (ch >> 1) & 1;
+        if (!wait(sh.bars.scores[turn], ph)) break;
         tc_fence_after();
-        int e;
-        {
-          // gamma^(i-j) q_i . k_j of a block of 32 columns, without the row's factor.  Before the
-          // warp's rows it is that factor times a column's, both at most 1; across them, from the
-          // table.  Not a product with 0: the score of a later token may be anything.
-          auto scores = [&](int b, float (&x)[32]) {
+        // The row's power of two, from the undecayed scores of the tokens up to it: the decayed
+        // ones are no larger, and far smaller only where fp16 has range to spare.
+        float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int b = b0; b <= b1; ++b) {
+          uint32_t d[32];
+          tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
+          tc_wait_ld();
+          if (b == q) {   // not the scores of later tokens, which may be anything
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (back ? j < lane : j > lane) d[j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(__uint_as_float(d[j])));
+        }
+        const int e = up_to_half(max4(top) * fabsf(w.a));
+        // ascending blocks: the packed columns of a block lie on blocks that are done with
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          uint32_t u[16];
+          if (b >= b0 && b <= b1) {
             uint32_t d[32];
             tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
             tc_wait_ld();
+            const float f = row_factor(b) * pow2(e);
             if (b != q) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&sh.col[j]);
-                x[j] = __uint_as_float(d[j]) * f.x;
-                x[j + 1] = __uint_as_float(d[j + 1]) * f.y;
-                x[j + 2] = __uint_as_float(d[j + 2]) * f.z;
-                x[j + 3] = __uint_as_float(d[j + 3]) * f.w;
+                const float4 c4 = *reinterpret_cast<const float4*>(&sh.col[j]);
+                u[j / 2] = pack2(__uint_as_float(d[j]) * (c4.x * f), __uint_as_float(d[j + 1]) * (c4.y * f));
+                u[j / 2 + 1] = pack2(__uint_as_float(d[j + 2]) * (c4.z * f), __uint_as_float(d[j + 3]) * (c4.w * f));
               }
-            } else if (back) {
-              const float* pw = sh.pow - lane;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = j >= lane ? __uint_as_float(d[j]) * pw[j] : 0.0f;
             } else {
-              const float* pw = sh.pow + lane;
+              // the table has zeros before gamma^0; and not a product with a later token's score
+              const float* pw = back ? sh.pow - lane : sh.pow + lane;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = j <= lane ? __uint_as_float(d[j]) * pw[-j] : 0.0f;
+              for (int j = 0; j < 32; j += 2) {
+                const float p0 = (back ? pw[j] : pw[-j]) * f, p1 = (back ? pw[j + 1] : pw[-j - 1]) * f;
+                const float x0 = (back ? j < lane : j > lane) ? 0.0f : __uint_as_float(d[j]);
+                const float x1 = (back ? j + 1 < lane : j + 1 > lane) ? 0.0f : __uint_as_float(d[j + 1]);
+                u[j / 2] = pack2(x0 * p0, x1 * p1);
+              }
             }
-          };
-          auto row_factor = [&](int b) {
-            return b == q ? w.a : w.a * sh.pow[back ? 32 * b - r : r - 32 * b - 31];
-          };
-          // two passes over TMEM, so that a block's values need not stay (and the loops need not be
-          // unrolled: their code would not fit the instruction cache beside the other roles')
-          const int b0 = back ? q : 0, b1 = back ? 3 : q;
-          float most = 0.0f;
-#pragma unroll 1
-          for (int b = b0; b <= b1; ++b) {
-            float x[32], top[4] = {0.f, 0.f, 0.f, 0.f};
-            scores(b, x);
+          } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(x[j]));
-            most = fmaxf(most, max4(top) * fabsf(row_factor(b)));
+            for (int j = 0; j < 16; ++j) u[j] = 0u;
           }
-          e = up_to_half(most);
-          // ascending blocks: the packed columns of a block lie on blocks that are done with
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            uint32_t u[16];
-            if (b >= b0 && b <= b1) {
-              float x[32];
-              scores(b, x);
-              const float f = row_factor(b) * pow2(e);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) u[j] = pack2(x[2 * j] * f, x[2 * j + 1] * f);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) u[j] = 0u;
-            }
-            st_x16(t_p + lane_addr + 16u * b, u);
-          }
-          tc_wait_st();
-          tc_fence_before();
-          // the state's exponent; its barrier cannot move on before P is handed over
-          if (!wait(sh.bars.state, ch & 1)) break;
-          arrive(sh.bars.p);
+          st_x16(t_p + lane_addr + 16u * b, u);
         }
-        if (!wait(sh.bars.out, ch & 1)) break;
+        tc_wait_st();
+        tc_fence_before();
+        if (!wait(sh.bars.state[turn], ph)) break;   // its exponent is read below
+        arrive(sh.bars.p[turn]);
+        if (!wait(sh.bars.out[turn], ph)) break;
         tc_fence_after();
         const float fi = w.b * sh.pow[i + 1 - lag] * pow2(-sh.exp_s[ch & 1]);
         const float fa = w.b * pow2(-e);
@@ -653,46 +678,34 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         __half* row = op + (row0(ch) + r) * w.o_t;
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          uint32_t x[32], y[32], bad_cols = 0u;
-          tc_ld_32x32b_x32(t_qs + lane_addr + 32u * b, x);
-          tc_ld_32x32b_x32(t_pv + lane_addr + 32u * b, y);
+        for (int b = 0; b < 8; ++b) {
+          uint32_t x[32], y[32];
+          tc_ld_32x32b_x16(t_qs + lane_addr + 16u * b, x);
+          tc_ld_32x32b_x16(t_pv + lane_addr + 16u * b, y);
           tc_wait_ld();
-          if (b == 3) {
+          if (b == 7) {
             tc_fence_before();
-            arrive(sh.bars.drained);
+            arrive(sh.bars.drained[turn]);
           }
-          if (bad) {
-#pragma unroll 1
-            for (int j = 0; j < 32; ++j)
-              if (ch * kC + i >= sh.bad_at[32 * b + j]) bad_cols |= 1u << j;
-          }
-          uint32_t u[16];
+          uint32_t u[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float o0 = fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa);
-            const float o1 = fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa);
-            u[j] = pack2(o0, o1);
-          }
-          if (bad_cols) {
+          for (int j = 0; j < 8; ++j)
+            u[j] = pack2(fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa),
+                         fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa));
+          if (bad) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              u[j] |= ((bad_cols >> (2 * j)) & 1u ? 0x7fffu : 0u) |
-                      ((bad_cols >> (2 * j + 1)) & 1u ? 0x7fff0000u : 0u);
+              if (ch * kC + i >= sh.bad_at[16 * b + j]) u[j / 2] |= (j & 1) ? 0x7fff0000u : 0x7fffu;
           }
           if (in) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              __half* p = row + 32 * b + 16 * j;
-              const uint32_t* z = u + 8 * j;
-              if (wide) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(z[0]),
-                             "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
-                             : "memory");
-              } else {
-                *reinterpret_cast<uint4*>(p) = make_uint4(z[0], z[1], z[2], z[3]);
-                *reinterpret_cast<uint4*>(p + 8) = make_uint4(z[4], z[5], z[6], z[7]);
-              }
+            __half* p = row + 16 * b;
+            if (wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+                           "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4*>(p + 8) = make_uint4(u[4], u[5], u[6], u[7]);
             }
           }
         }

@@ -156,6 +156,39 @@ def test_split_sequences(dt, d, cu):
     _check_forward(o, hT, q, k, v, _decays(H), cu or [0, T], 0.1, h0)
 
 
+# segments of many chunks: unsplit sequences (enough heads to fill the GPU), with and without a
+# state as an output, and split ones; a few heads against the plain form
+@pytest.mark.parametrize("T,H,split", [(1300, 300, False), (2700, 40, True)])
+@pytest.mark.parametrize("d,state", [(128, True), (128, False), (64, True)])
+def test_long_segments(T, H, split, d, state):
+    heads = [0, 5, H - 1]
+    g = torch.Generator(device=DEV).manual_seed(H)
+    q, k, v = (torch.randn(T, H, d, generator=g, device=DEV).half() for _ in range(3))
+    do = torch.randn(T, H, d, generator=g, device=DEV).half()
+    lg, hT = _decays(H), torch.empty(1, H, d, d, device=DEV) if state else None
+    assert (mmf.mmf_linattn_workspace_bytes(mmf._linattn(q, k, v, to_dev(lg), None, None, None,
+                                                         None)) > 0) == split or d == 64
+    o = mmf.linattn_forward(q, k, v, to_dev(lg), hT=hT)
+    grads = mmf.linattn_backward(q, k, v, to_dev(lg), do, want_dh0=state)
+    torch.cuda.synchronize()
+    assert mmf.mmf_get_device_status() == 0
+    a = [x[:, heads].cpu().numpy() for x in (q, k, v, do)]
+    ref, refT = plain.linattn(*a[:3], lg[heads], [0, T], d ** -0.5)
+    mag, magT = plain.absolute(plain.linattn, *a[:3], lg[heads], [0, T], d ** -0.5)
+    got = o[:, heads].cpu().numpy()
+    plain.assert_close(got, ref, plain.tolerance(ref, mag, True, T, d), "o")
+    plain.assert_norm(got, ref, 2 * plain.U16, "o")
+    if state:
+        got = hT[:, heads].cpu().numpy()
+        plain.assert_close(got, refT, plain.sum_bound(T, d) * magT, "hT")
+        plain.assert_norm(got, refT, 2e-6, "hT")
+    grads = [x if x is None else x[:, heads] for x in grads]
+    ref = plain.linattn_backward(*a[:3], lg[heads], [0, T], d ** -0.5, a[3])
+    for name, x, r in zip(("dq", "dk", "dv", "dh0"), grads, ref):
+        if x is not None:
+            plain.assert_norm(x.cpu().numpy(), r, 2e-6 if name == "dh0" else 2 * plain.U16, name)
+
+
 @pytest.mark.parametrize("dt", [np.float16, np.float32])
 def test_equal_batches_and_in_place_states(dt):
     T, H, d, B = 1800, 2, 64, 3
