@@ -67,27 +67,6 @@ struct Lay {
   static constexpr int kCols = kState ? 128 : 512;
 };
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // kind::f16, fp32 accumulator, fp16 operands, M = N = 128; bits 15 and 16: A and B MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(bool a_mn, bool b_mn) {
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((kD / 8) << 17) |
@@ -107,33 +86,83 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
   return d;
 }
 
-// Both K-major: contraction over the 64 + 64 values of the two panels' rows.
+// Products of 128 x 128 x 128: eight MMAs of depth 16, issued by one elected lane of a converged
+// warp.  Offsets are in 16-byte units of shared memory (TMEM: columns).
+// Both K-major: 16 values are 32 bytes of a row, 64 a panel.
 __device__ __forceinline__ void product_kk(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t idesc = idesc_f16(false, false);
-  const uint64_t ad = smem_desc_kmajor_sw128(a), bd = smem_desc_kmajor_sw128(b);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint64_t off = static_cast<uint64_t>(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
-    mma_ss(d, ad + off, bd + off, idesc, k > 0 ? 1u : 0u);
-  }
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b;\n\t.reg .b64 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+      "l"(smem_desc_kmajor_sw128(a)), "l"(smem_desc_kmajor_sw128(b)), "r"(idesc_f16(false, false)), "r"(0)
+      : "memory");
 }
-// Both MN-major: contraction over the tiles' 128 rows.
-__device__ __forceinline__ void product_mn(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr uint32_t idesc = idesc_f16(true, true);
-  const uint64_t ad = desc_mn(a), bd = desc_mn(b);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint64_t off = static_cast<uint64_t>((k * 16 * 128) >> 4);
-    mma_ss(d, ad + off, bd + off, idesc, (k > 0 || add) ? 1u : 0u);
-  }
+// Both MN-major: contraction over the tiles' 128 rows, 16 of them 2048 bytes.
+__device__ __forceinline__ void product_mn(uint32_t d, uint32_t a, uint32_t b, int add) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b;\n\t.reg .b64 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 128;\n\tadd.s64 b, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 256;\n\tadd.s64 b, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 384;\n\tadd.s64 b, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 512;\n\tadd.s64 b, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 640;\n\tadd.s64 b, %2, 640;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 768;\n\tadd.s64 b, %2, 768;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 896;\n\tadd.s64 b, %2, 896;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+      "l"(desc_mn(a)), "l"(desc_mn(b)), "r"(idesc_f16(true, true)), "r"(add)
+      : "memory");
 }
 // A in TMEM (16 fp16 are eight columns), B MN-major.
 __device__ __forceinline__ void product_tm(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t idesc = idesc_f16(false, true);
-  const uint64_t bd = desc_mn(b);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    mma_ts(d, a + 8u * k, bd + static_cast<uint64_t>((k * 16 * 128) >> 4), idesc, k > 0 ? 1u : 0u);
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 32;\n\tadd.s64 b, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 40;\n\tadd.s64 b, %2, 640;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 48;\n\tadd.s64 b, %2, 768;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 56;\n\tadd.s64 b, %2, 896;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(desc_mn(b)), "r"(idesc_f16(false, true)), "r"(0)
+      : "memory");
+}
+
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float v;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
 }
 
 __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -178,23 +207,32 @@ struct LinMaps {
   CUtensorMap m[3 * kMaxSweeps];
 };
 
-// A bounded wait that looks at the clock only once in many tries: the roles hand over to one
-// another several times a chunk, and a read of the global timer in that path costs microseconds.
+// A wait of at most kTries tries, each of which may suspend the warp for up to kTryNs, so that
+// waiting warps leave the issue slots and the shared-memory pipe to the working ones.
+constexpr int kTries = 1 << 17;
+constexpr uint32_t kTryNs = 20000;
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
                                              unsigned* status) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+  int left = kTries;
+  while (!try_wait(bar, parity)) {
+    if (--left == 0) {
       *abort = 1;
       atomicOr(status, kStatusTimeout);
-      return false;
     }
+    if (*abort) return false;
   }
+  return true;
 }
 
 // A wait names a phase by its parity, so whoever waits must come before the phase after the next
@@ -448,8 +486,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         ok = wait(sh.bars.k[s], ph) && (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        product_mn(t_upd, tile_v(s), tile_k(s), false);
-        product_mn(t_upd, tile_v(s), tile_q(s), true);
+        product_mn(t_upd, tile_v(s), tile_k(s), 0);
+        product_mn(t_upd, tile_v(s), tile_q(s), 1);
         commit(sh.bars.upd);
       } else {
         // scores, in P's place: the product that read it last has completed
@@ -468,8 +506,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph);
         if (!ok) break;
         tc_fence_after();
-        product_mn(t_upd, tile_v(s), tile_k(s), false);
-        if (two) product_mn(t_upd, tile_v(s), tile_q(s), true);
+        product_mn(t_upd, tile_v(s), tile_k(s), 0);
+        if (two) product_mn(t_upd, tile_v(s), tile_q(s), 1);
         commit(sh.bars.upd);
         ok = wait(sh.bars.p[s], ph);
         if (!ok) break;
@@ -490,7 +528,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
     const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * kD * kD;
     float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * kD * kD : nullptr;
-    float S[kD];
+    uint64_t S[kD / 2];                            // pairs of values
     {
       const float* from = nullptr;
       size_t sk = kD, sv = 1;
@@ -502,12 +540,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         sv = static_cast<size_t>(w.s_val);
       }
 #pragma unroll
-      for (int i = 0; i < kD; ++i) S[i] = from ? from[i * sk + r * sv] : 0.0f;
+      for (int i = 0; i < kD / 2; ++i)
+        S[i] = from ? pair(from[2 * i * sk + r * sv], from[(2 * i + 1) * sk + r * sv]) : 0ull;
     }
     float top[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (!kState) {
 #pragma unroll
-      for (int i = 0; i < kD; ++i) top[i & 3] = fmaxf(top[i & 3], fabsf(S[i]));
+      for (int i = 0; i < kD / 2; ++i) {
+        const float2 x = unpair(S[i]);
+        top[i & 3] = max3_abs(top[i & 3], x.x, x.y);
+      }
     }
     // the state for chunk ch: scaled, rounded and written as the B operand of Q S
     auto publish = [&](int ch, bool ok) {
@@ -516,12 +558,17 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       if (!named_bar_and(1, kGroup, ok)) return false;
       const int e = up_to_half(max4(sh.red_s));
       if (r == 0) sh.exp_s[ch & 1] = e;
-      const float f = pow2(e);
+      const uint64_t f2 = pair(pow2(e), pow2(e));
 #pragma unroll
-      for (int x = 0; x < 16; ++x)
-        sts128(vec_at(tile_s, r, x),
-               make_uint4(pack2(S[8 * x] * f, S[8 * x + 1] * f), pack2(S[8 * x + 2] * f, S[8 * x + 3] * f),
-                          pack2(S[8 * x + 4] * f, S[8 * x + 5] * f), pack2(S[8 * x + 6] * f, S[8 * x + 7] * f)));
+      for (int x = 0; x < 16; ++x) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = unpair(mul2(S[4 * x + i], f2));
+          u[i] = pack2(y.x, y.y);
+        }
+        sts128(vec_at(tile_s, r, x), make_uint4(u[0], u[1], u[2], u[3]));
+      }
       fence_proxy_async_smem();
       arrive(sh.bars.state[ch & 1]);
       return true;
@@ -533,6 +580,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       if (w2) {
         tc_fence_after();
         const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[ch & 3]);
+        const uint64_t decay2 = pair(decay, decay), f2 = pair(f, f);
         top[0] = top[1] = top[2] = top[3] = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -540,10 +588,13 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
           tc_ld_32x32b_x32(t_upd + lane_addr + 32u * b, d);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float& x = S[32 * b + i];
-            x = fmaf(decay, x, __uint_as_float(d[i]) * f);
-            if constexpr (!kState) top[i & 3] = fmaxf(top[i & 3], fabsf(x));
+          for (int i = 0; i < 16; ++i) {
+            uint64_t& x = S[16 * b + i];
+            x = fma2(decay2, x, mul2(pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), f2));
+            if constexpr (!kState) {
+              const float2 y = unpair(x);
+              top[i & 3] = max3_abs(top[i & 3], y.x, y.y);
+            }
           }
         }
         tc_fence_before();
@@ -563,7 +614,11 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       const size_t sv = kState ? 1 : static_cast<size_t>(w.s_val);
       const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) && sh.bad_at[r] != 0x7fffffff;
 #pragma unroll
-      for (int i = 0; i < kD; ++i) to[i * sk + r * sv] = bad ? __int_as_float(0x7fffffff) : S[i];
+      for (int i = 0; i < kD / 2; ++i) {
+        const float2 x = unpair(S[i]);
+        to[2 * i * sk + r * sv] = bad ? __int_as_float(0x7fffffff) : x.x;
+        to[(2 * i + 1) * sk + r * sv] = bad ? __int_as_float(0x7fffffff) : x.y;
+      }
     }
   } else if (warp < 12) {
     // --------------------------------------------------------------------------- K to K'
@@ -630,7 +685,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
               if (back ? j < lane : j > lane) d[j] = 0u;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(__uint_as_float(d[j])));
+          for (int j = 0; j < 16; ++j)
+            top[j & 3] = max3_abs(top[j & 3], __uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
         }
         const int e = up_to_half(max4(top) * fabsf(w.a));
         // ascending blocks: the packed columns of a block lie on blocks that are done with
@@ -643,11 +699,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
             tc_wait_ld();
             const float f = row_factor(b) * pow2(e);
             if (b != q) {
+              const uint64_t f2 = pair(f, f);
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const float4 c4 = *reinterpret_cast<const float4*>(&sh.col[j]);
-                u[j / 2] = pack2(__uint_as_float(d[j]) * (c4.x * f), __uint_as_float(d[j + 1]) * (c4.y * f));
-                u[j / 2 + 1] = pack2(__uint_as_float(d[j + 2]) * (c4.z * f), __uint_as_float(d[j + 3]) * (c4.w * f));
+                const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(&sh.col[j]);
+                const float2 x = unpair(mul2(pair(__uint_as_float(d[j]), __uint_as_float(d[j + 1])),
+                                             mul2(c4.x, f2)));
+                const float2 y = unpair(mul2(pair(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])),
+                                             mul2(c4.y, f2)));
+                u[j / 2] = pack2(x.x, x.y);
+                u[j / 2 + 1] = pack2(y.x, y.y);
               }
             } else {
               // the table has zeros before gamma^0; and not a product with a later token's score
@@ -674,6 +735,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         tc_fence_after();
         const float fi = w.b * sh.pow[i + 1 - lag] * pow2(-sh.exp_s[ch & 1]);
         const float fa = w.b * pow2(-e);
+        const uint64_t fi2 = pair(fi, fi), fa2 = pair(fa, fa);
         const bool in = i < tokens(ch);
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         __half* row = op + (row0(ch) + r) * w.o_t;
@@ -690,8 +752,12 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
           uint32_t u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            u[j] = pack2(fmaf(__uint_as_float(x[2 * j]), fi, __uint_as_float(y[2 * j]) * fa),
-                         fmaf(__uint_as_float(x[2 * j + 1]), fi, __uint_as_float(y[2 * j + 1]) * fa));
+          {
+            const float2 o = unpair(
+                fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fi2,
+                     mul2(pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), fa2)));
+            u[j] = pack2(o.x, o.y);
+          }
           if (bad) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
