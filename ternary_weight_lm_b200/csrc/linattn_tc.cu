@@ -197,9 +197,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// 16-byte vector x (0..15) of row r of a two-panel tile
-__device__ __forceinline__ uint32_t vec_at(uint32_t tile, int r, int x) {
-  return tile + static_cast<uint32_t>((x >> 3) * kPanel + r * 128 + (((x & 7) ^ (r & 7)) << 4));
+// Row r of a two-panel tile, and its 16-byte vector x (0..15): in a swizzled row of 128 bytes vector
+// x is at x ^ (r mod 8), so that its address is the row's with three bits flipped.
+__device__ __forceinline__ uint32_t row_at(uint32_t tile, int r) {
+  return tile + static_cast<uint32_t>(r * 128 + ((r & 7) << 4));
+}
+__device__ __forceinline__ uint32_t vec_of(uint32_t row, int x) {
+  return (row ^ static_cast<uint32_t>((x & 7) << 4)) + static_cast<uint32_t>((x >> 3) * kPanel);
 }
 
 // Tensor maps of each sweep's k, v and q.
@@ -248,10 +252,10 @@ struct Bars {
 
 struct Shared {
   Bars bars;
-  float zeros[32];          // pow[-32] .. pow[-1]: the factor of a later token's score
   float pow[kC + 4];        // gamma^0 .. gamma^128
+  float diag[64];           // diag[32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i
   alignas(16) float col[32];   // gamma^(31-j) forwards, gamma^j backwards
-  float red_k[2][4], red_w[2][4], red_s[4];
+  float red_k[2][4], red_w[2][4], top_k[2][4], red_s[4];
   int exp_s[2];             // exponent of the fp16 state, by chunk
   int exp_k[4];             // of K'
   int bad_at[kD];           // first position of the segment whose v is not finite, by column
@@ -310,8 +314,11 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (!kState) tma_prefetch_desc(mq);
   }
   if (tid <= kC) sh.pow[tid] = lin_power(lin_lg2(c, h), tid);
+  if (tid < 64) {
+    const int d = back ? tid - 32 : 32 - tid;
+    sh.diag[tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
+  }
   if (tid < 32) {
-    sh.zeros[tid] = 0.0f;
     sh.col[tid] = lin_power(lin_lg2(c, h), back ? tid : 31 - tid);
   }
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
@@ -342,22 +349,22 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     return static_cast<int>(min(static_cast<int64_t>(kC), g.n - static_cast<int64_t>(chunk) * kC));
   };
 
-  // Thread r of a group of four warps (named barrier `id`): row r of V made safe for the products:
-  // zeros where the row is no token of the segment and where a value is not finite.
+  // Thread r of a group of four warps: row r of V made safe for the products: zeros where the row is
+  // no token of the segment and where a value is not finite.
   auto clean_v = [&](int chunk, int r) {
-    const int s = chunk & 1, pos = back ? kC - 1 - r : r;
-    const uint32_t t = tile_v(s);
+    const int pos = back ? kC - 1 - r : r;
+    const uint32_t row = row_at(tile_v(chunk & 1), r);
     if (pos >= tokens(chunk)) {
 #pragma unroll 1
-      for (int x = 0; x < 16; ++x) sts128(vec_at(t, r, x), make_uint4(0u, 0u, 0u, 0u));
+      for (int x = 0; x < 16; ++x) sts128(vec_of(row, x), make_uint4(0u, 0u, 0u, 0u));
     } else {
       // 0 times what is not finite is NaN
       __half2 odd[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) odd[e] = __float2half2_rn(0.0f);
-#pragma unroll 8
+#pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const uint4 v = lds128(vec_at(t, r, x));
+        const uint4 v = lds128(vec_of(row, x));
         const __half2* hv = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) odd[e] = __hfma2(hv[e], __float2half2_rn(0.0f), odd[e]);
@@ -366,7 +373,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       if (!(sum.x + sum.y == 0.0f)) {
 #pragma unroll 1
         for (int col = 0; col < kD; ++col) {
-          const uint32_t a = vec_at(t, r, col >> 3) + 2u * (col & 7);
+          const uint32_t a = vec_of(row, col >> 3) + 2u * (col & 7);
           uint16_t x;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
           if ((x & 0x7c00u) == 0x7c00u) {
@@ -383,34 +390,39 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   // chunk's power of two.  With the factor w 2^e = wh + wl in fp16, hi = k wh rounded, and the rest
   // (k wh - hi, exact, plus k wl) is lo: three half2 operations, an error of about 2^-22.  e brings
   // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
-  // that is less.  False if one of the group's warps gave up (`ok`).
+  // that is less.
+  // Largest magnitude in row r of a tile of K or Q, infinity or NaN if one of it is not finite.
+  auto row_top = [&](uint32_t tile, int r) {
+    const uint32_t row = row_at(tile, r);
+    __half2 m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const uint4 v = lds128(vec_of(row, x));
+      const __half2* hv = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = __hmax2_nan(m[e], __habs2(hv[e]));
+    }
+    const float2 y = __half22float2(__hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3])));
+    return y.x >= y.y || y.x != y.x ? y.x : y.y;
+  };
   // find_exp: e and the row's factor; false if one of the group's warps gave up (`ok`).
   auto find_exp = [&](int chunk, int r, int id, bool ok, float* f) {
     const int set = chunk & 1;   // written again only after the whole group handed the chunk over
     const int n = tokens(chunk), pos = back ? kC - 1 - r : r;
-    const uint32_t t = tile_k(chunk & 1);
     const bool in = pos < n;
     const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
     float top = 0.0f;
-    if (ok && in) {
-      __half2 m[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.0f);
-#pragma unroll 8
-      for (int x = 0; x < 16; ++x) {
-        const uint4 v = lds128(vec_at(t, r, x));
-        const __half2* hv = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(hv[e]));
-      }
-      const float2 y = __half22float2(__hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3])));
-      top = fmaxf(y.x, y.y);
-    }
+    if (ok && in) top = row_top(tile_k(chunk & 1), r);
+    if (!(top <= 65504.0f)) sh.any_bad = 1;
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
+    const float most = warp_max(top);
     top = warp_max(top * fabsf(wt));
     if (lane == 0) {
       sh.red_k[set][r >> 5] = top;
       sh.red_w[set][r >> 5] = wide;
+      sh.top_k[set][r >> 5] = most;
     }
     if (!named_bar_and(id, kGroup, ok)) return false;
     const int e = min(up_to_half(max4(sh.red_k[set])), up_to_half(max4(sh.red_w[set])));
@@ -419,28 +431,31 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     return true;
   };
   auto decay_k = [&](int chunk, int r, float f, bool two) {
-    const uint32_t t = tile_k(chunk & 1), t2 = tile_q(chunk & 1);
+    const uint32_t row = row_at(tile_k(chunk & 1), r), row2 = row_at(tile_q(chunk & 1), r);
     const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
     const __half fh = __float2half_rn(f);
     const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
-#pragma unroll 1
-    for (int x0 = 0; x0 < 16; x0 += 4) {
-      uint4 v[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[x] = in ? lds128(vec_at(t, r, x0 + x)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int x0 = 0; x0 < 16; x0 += 8) {
+      uint4 v[8];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < 8; ++x) v[x] = lds128(vec_of(row, x0 + x));
+      if (!in)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
         uint4 hi, lo;
         const __half2* k2 = reinterpret_cast<const __half2*>(&v[x]);
         __half2* h2 = reinterpret_cast<__half2*>(&hi);
         __half2* l2 = reinterpret_cast<__half2*>(&lo);
 #pragma unroll
         for (int i = 0; i < 4; ++i) h2[i] = __hmul2(k2[i], wh);
-        sts128(vec_at(t, r, x0 + x), hi);
+        sts128(vec_of(row, x0 + x), hi);
         if (two) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
-          sts128(vec_at(t2, r, x0 + x), lo);
+          sts128(vec_of(row2, x0 + x), lo);
         }
       }
     }
@@ -559,6 +574,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       const int e = up_to_half(max4(sh.red_s));
       if (r == 0) sh.exp_s[ch & 1] = e;
       const uint64_t f2 = pair(pow2(e), pow2(e));
+      const uint32_t s_row = row_at(tile_s, r);
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         uint32_t u[4];
@@ -567,7 +583,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
           const float2 y = unpair(mul2(S[4 * x + i], f2));
           u[i] = pack2(y.x, y.y);
         }
-        sts128(vec_at(tile_s, r, x), make_uint4(u[0], u[1], u[2], u[3]));
+        sts128(vec_of(s_row, x), make_uint4(u[0], u[1], u[2], u[3]));
       }
       fence_proxy_async_smem();
       arrive(sh.bars.state[ch & 1]);
@@ -628,12 +644,10 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       for (int ch = 0; ch < chunks; ++ch) {
         const int s = ch & 1, ph = (ch >> 1) & 1;
         bool ok = wait(sh.bars.full[s], ph);
-        if (ok) {
-          clean_v(ch, r);
-          arrive(sh.bars.v[s]);
-        }
+        if (ok) clean_v(ch, r);
         float f;
         if (!find_exp(ch, r, 2, ok, &f)) break;
+        arrive(sh.bars.v[s]);
         // K, and with two parts Q, are no longer read as such
         ok = two ? wait(sh.bars.qk, ch & 1) : wait(sh.bars.scores[s], ph);
         if (!ok) break;
@@ -669,26 +683,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       };
       for (int ch = turn; ch < chunks; ch += 2) {
         const int ph = (ch >> 1) & 1;
+        // The row's power of two, from a bound on its scores, 128 max|q_i| max|k|: a few bits more
+        // than they have, of the 29 between fp16's largest and smallest normal values.
+        if (!wait(sh.bars.full[turn], ph)) break;
+        const float top_q = row_top(tile_q(turn), r);
+        if (!wait(sh.bars.v[turn], ph)) break;
+        const int e = up_to_half(top_q * max4(sh.top_k[turn]) * (128.0f * fabsf(w.a)));
+        const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
+        const bool bad_k = bad || tokens(ch) < kC;   // rows past the end may hold anything
         if (!wait(sh.bars.scores[turn], ph)) break;
         tc_fence_after();
-        // The row's power of two, from the undecayed scores of the tokens up to it: the decayed
-        // ones are no larger, and far smaller only where fp16 has range to spare.
-        float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int b = b0; b <= b1; ++b) {
-          uint32_t d[32];
-          tc_ld_32x32b_x32(t_p + lane_addr + 32u * b, d);
-          tc_wait_ld();
-          if (b == q) {   // not the scores of later tokens, which may be anything
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (back ? j < lane : j > lane) d[j] = 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            top[j & 3] = max3_abs(top[j & 3], __uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
-        }
-        const int e = up_to_half(max4(top) * fabsf(w.a));
         // ascending blocks: the packed columns of a block lie on blocks that are done with
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
@@ -711,15 +715,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
                 u[j / 2 + 1] = pack2(y.x, y.y);
               }
             } else {
-              // the table has zeros before gamma^0; and not a product with a later token's score
-              const float* pw = back ? sh.pow - lane : sh.pow + lane;
+              if (bad_k) {
+                // not a product with 0: the score of a later token may be anything
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float p0 = (back ? pw[j] : pw[-j]) * f, p1 = (back ? pw[j + 1] : pw[-j - 1]) * f;
-                const float x0 = (back ? j < lane : j > lane) ? 0.0f : __uint_as_float(d[j]);
-                const float x1 = (back ? j + 1 < lane : j + 1 > lane) ? 0.0f : __uint_as_float(d[j + 1]);
-                u[j / 2] = pack2(x0 * p0, x1 * p1);
+                for (int j = 0; j < 32; ++j)
+                  if (back ? j < lane : j > lane) d[j] = 0u;
               }
+              const float* pw = sh.diag + 32 - lane;
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                u[j / 2] = pack2(__uint_as_float(d[j]) * (pw[j] * f), __uint_as_float(d[j + 1]) * (pw[j + 1] * f));
             }
           } else {
 #pragma unroll
@@ -737,7 +742,6 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         const float fa = w.b * pow2(-e);
         const uint64_t fi2 = pair(fi, fi), fa2 = pair(fa, fa);
         const bool in = i < tokens(ch);
-        const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         __half* row = op + (row0(ch) + r) * w.o_t;
 #pragma unroll 1
         for (int b = 0; b < 8; ++b) {
