@@ -494,23 +494,30 @@ class _On:
         import torch
         if t.device.type != "cuda":
             raise ValueError(f"tensors must be on a GPU, got {t.device}")
-        self.device = torch.cuda.device(t.device)
+        self.device = self.stream = None
+        if t.device.index != torch.cuda.current_device():
+            self.device = torch.cuda.device(t.device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=t.device)
         self.given = stream
 
     def __enter__(self):
         import torch
-        self.device.__enter__()
-        s = torch.cuda.current_stream() if self.given is None else self.given
-        self.stream = torch.cuda.stream(s)
-        self.stream.__enter__()
-        self.handle = s.cuda_stream
+        if self.device is not None:
+            self.device.__enter__()
+        if self.given is not None:
+            self.stream = torch.cuda.stream(self.given)
+            self.stream.__enter__()
+            self.handle = self.given.cuda_stream
+        else:
+            self.handle = torch.cuda.current_stream().cuda_stream
         return self
 
     def __exit__(self, *exc):
-        self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
 
 
 def quantize_weights_int8(W, stream=None):

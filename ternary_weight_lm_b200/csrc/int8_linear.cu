@@ -311,11 +311,27 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
       const int n = n0 + r;
       const uint32_t part0 = smem_u32(smem);
       const float ws = n < p.N ? p.wscale[n] : 0.0f;
-      for (int j = static_cast<int>(cluster_ctarank()); j < BN && t0 + j < p.T; j += csize) {
-        int32_t v = 0;   // exact, so the order of the blocks does not matter
-        for (int c = 0; c < csize; ++c)
-          v += ld_cluster_s32(map_peer(part0 + 4u * static_cast<uint32_t>(j * kRows + r), c));
-        if (n < p.N) put(p, t0 + j, n, v, s_gam[j] * ws);
+      // eight tokens at a time, so that their loads from the other blocks overlap
+      constexpr int kAtOnce = 8;
+      const int live = static_cast<int>(min(static_cast<int64_t>(BN), p.T - t0));
+      for (int j0 = static_cast<int>(cluster_ctarank()); j0 < live; j0 += csize * kAtOnce) {
+        int32_t v[kAtOnce];   // exact, so the order of the blocks does not matter
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) v[u] = 0;
+        for (int c = 0; c < csize; ++c) {
+          const uint32_t from = map_peer(part0 + 4u * static_cast<uint32_t>(j0 * kRows + r), c);
+          int32_t x[kAtOnce];
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u)
+            x[u] = j0 + u * csize < live ? ld_cluster_s32(from + 4u * static_cast<uint32_t>(u * csize * kRows)) : 0;
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) v[u] += x[u];
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int j = j0 + u * csize;
+          if (j < live && n < p.N) put(p, t0 + j, n, v[u], s_gam[j] * ws);
+        }
       }
     }
     cluster_sync_all();   // the partial sums stay readable until everyone is done
@@ -399,7 +415,17 @@ cudaError_t launch_quantize_weights_i8(const void* W, int wdt, int64_t N, int K,
   return cudaGetLastError();
 }
 
+// Which contraction.  The CTA-pair pipeline takes 256 x 256 tiles over the whole of K (about 5 us
+// plus 0.27 us for each k-block of 128 and round of 74 tiles); this file's splits K over a cluster
+// when its 128-row tiles are few.  Measured (us, here / pairs): T 129, K 5632, N 2048 12.1 / 17.1;
+// T 512, K 8192, N 1024 14.1 / 22.7; T 256, K 4096, N 4096 12.9 / 14.3; but T 512, K 4096, N 4096
+// 16.6 / 14.9; T 256, K 2048, N 2048 11.2 / 9.6; T 128, K 2048, N 11264 13.0 / 11.1; T 64, K 2048,
+// N 11264 9.9 / 11.2.  So: up to 64 tokens here; beyond, here only for a deep K that at least four
+// blocks can share.
 cudaError_t launch_int8_linear(const Int8Call& c, cudaStream_t s) {
+  const int64_t tiles = ((c.N + kRows - 1) / kRows) * ((c.T + 127) / 128);
+  const int nkb = (c.K + kKB - 1) / kKB;
+  if (c.T > 64 && !(nkb >= 28 && 4 * tiles <= kSlots)) return launch_int8_pairs(c, s);
   if (c.T <= 16) return launch_bn<16>(c, s);
   if (c.T <= 32) return launch_bn<32>(c, s);
   if (c.T <= 64) return launch_bn<64>(c, s);

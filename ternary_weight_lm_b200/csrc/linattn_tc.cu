@@ -31,7 +31,7 @@
 // outputs and state are NaN.
 //
 // kState: the state alone (pass one of a split sequence).  There the tokens' two groups turn K into
-// K', in turns, and the group for it idles.
+// K', a panel of 64 columns each, and the group for it looks after V.
 //
 // Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
 // copies and MMAs in flight are drained and TMEM is freed.
@@ -186,6 +186,9 @@ __device__ __forceinline__ int up_to_half(float top) {
 __device__ __forceinline__ float warp_max(float magnitude) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(magnitude)));
 }
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
 __device__ __forceinline__ float max4(const float (&x)[4]) {
   return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 }
@@ -255,7 +258,7 @@ struct Shared {
   float pow[kC + 4];        // gamma^0 .. gamma^128
   float diag[64];           // diag[32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i
   alignas(16) float col[32];   // gamma^(31-j) forwards, gamma^j backwards
-  float red_k[2][4], red_w[2][4], top_k[2][4], red_s[4];
+  float red_k[2][8], red_w[2][8], top_k[2][8], red_s[4];   // of each warp (a panel's four)
   int exp_s[2];             // exponent of the fp16 state, by chunk
   int exp_k[4];             // of K'
   int bad_at[kD];           // first position of the segment whose v is not finite, by column
@@ -299,7 +302,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       mbar_init(smem_u32(&sh.bars.p[s]), 4);
       mbar_init(smem_u32(&sh.bars.out[s]), 1);
       mbar_init(smem_u32(&sh.bars.drained[s]), 4);
-      mbar_init(smem_u32(&sh.bars.k[s]), 4);
+      mbar_init(smem_u32(&sh.bars.k[s]), kState ? 8 : 4);
       mbar_init(smem_u32(&sh.bars.v[s]), 4);
       mbar_init(smem_u32(&sh.bars.state[s]), 4);
     }
@@ -322,6 +325,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     sh.col[tid] = lin_power(lin_lg2(c, h), back ? tid : 31 - tid);
   }
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
+  if (tid < 16) sh.red_k[tid >> 3][tid & 7] = sh.red_w[tid >> 3][tid & 7] = sh.top_k[tid >> 3][tid & 7] = 0.0f;
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), L::kCols);
     tmem_relinquish();
@@ -392,13 +396,13 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
   // that is less.
   // Largest magnitude in row r of a tile of K or Q, infinity or NaN if one of it is not finite.
-  auto row_top = [&](uint32_t tile, int r) {
-    const uint32_t row = row_at(tile, r);
+  constexpr int kVecs = kState ? 8 : 16;   // vectors of a row that a thread takes (kState: a panel)
+  auto row_top = [&](uint32_t row) {
     __half2 m[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.0f);
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
+    for (int x = 0; x < kVecs; ++x) {
       const uint4 v = lds128(vec_of(row, x));
       const __half2* hv = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
@@ -407,36 +411,39 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float2 y = __half22float2(__hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3])));
     return y.x >= y.y || y.x != y.x ? y.x : y.y;
   };
-  // find_exp: e and the row's factor; false if one of the group's warps gave up (`ok`).
-  auto find_exp = [&](int chunk, int r, int id, bool ok, float* f) {
-    const int set = chunk & 1;   // written again only after the whole group handed the chunk over
+  // find_exp: e and row r's factor; false if one of the warps gave up (`ok`).  Named barrier `id` is
+  // that of the threads that share the tile: a group, or two with a panel each.
+  auto find_exp = [&](int chunk, int r, int panel, int id, bool ok, float* f) {
+    const int set = chunk & 1;   // written again only after all of them handed the chunk over
     const int n = tokens(chunk), pos = back ? kC - 1 - r : r;
     const bool in = pos < n;
     const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
     float top = 0.0f;
-    if (ok && in) top = row_top(tile_k(chunk & 1), r);
+    if (ok && in) top = row_top(row_at(tile_k(chunk & 1) + panel * kPanel, r));
     if (!(top <= 65504.0f)) sh.any_bad = 1;
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
     const float most = warp_max(top);
     top = warp_max(top * fabsf(wt));
     if (lane == 0) {
-      sh.red_k[set][r >> 5] = top;
-      sh.red_w[set][r >> 5] = wide;
-      sh.top_k[set][r >> 5] = most;
+      const int at = (r >> 5) + 4 * panel;
+      sh.red_k[set][at] = top;
+      sh.red_w[set][at] = wide;
+      sh.top_k[set][at] = most;
     }
-    if (!named_bar_and(id, kGroup, ok)) return false;
-    const int e = min(up_to_half(max4(sh.red_k[set])), up_to_half(max4(sh.red_w[set])));
-    if (r == 0) sh.exp_k[chunk & 3] = e;
+    if (!named_bar_and(id, kState ? 2 * kGroup : kGroup, ok)) return false;
+    const int e = min(up_to_half(max8(sh.red_k[set])), up_to_half(max8(sh.red_w[set])));
+    if (r == 0 && panel == 0) sh.exp_k[chunk & 3] = e;
     *f = wt * pow2(e);
     return true;
   };
-  auto decay_k = [&](int chunk, int r, float f, bool two) {
-    const uint32_t row = row_at(tile_k(chunk & 1), r), row2 = row_at(tile_q(chunk & 1), r);
+  auto decay_k = [&](int chunk, int r, int panel, float f, bool two) {
+    const uint32_t row = row_at(tile_k(chunk & 1) + panel * kPanel, r);
+    const uint32_t row2 = row_at(tile_q(chunk & 1) + panel * kPanel, r);
     const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
     const __half fh = __float2half_rn(f);
     const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
 #pragma unroll
-    for (int x0 = 0; x0 < 16; x0 += 8) {
+    for (int x0 = 0; x0 < kVecs; x0 += 8) {
       uint4 v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[x] = lds128(vec_of(row, x0 + x));
@@ -498,7 +505,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       const int s = ch & 1, ph = (ch >> 1) & 1;
       if constexpr (kState) {
         // K' and V are ready, and the update before is read
-        ok = wait(sh.bars.k[s], ph) && (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
+        ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph) &&
+             (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), 0);
@@ -639,19 +647,22 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   } else if (warp < 12) {
     // --------------------------------------------------------------------------- K to K'
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecay));
-    if constexpr (!kState) {
-      const int r = 32 * (warp & 3) + lane;
-      for (int ch = 0; ch < chunks; ++ch) {
-        const int s = ch & 1, ph = (ch >> 1) & 1;
-        bool ok = wait(sh.bars.full[s], ph);
-        if (ok) clean_v(ch, r);
+    const int r = 32 * (warp & 3) + lane;
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int s = ch & 1, ph = (ch >> 1) & 1;
+      bool ok = wait(sh.bars.full[s], ph);
+      if (ok) clean_v(ch, r);
+      if constexpr (kState) {
+        if (!ok) break;
+        arrive(sh.bars.v[s]);
+      } else {
         float f;
-        if (!find_exp(ch, r, 2, ok, &f)) break;
+        if (!find_exp(ch, r, 0, 2, ok, &f)) break;
         arrive(sh.bars.v[s]);
         // K, and with two parts Q, are no longer read as such
         ok = two ? wait(sh.bars.qk, ch & 1) : wait(sh.bars.scores[s], ph);
         if (!ok) break;
-        decay_k(ch, r, f, two);
+        decay_k(ch, r, 0, f, two);
         arrive(sh.bars.k[s]);
       }
     }
@@ -660,14 +671,12 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int q = warp & 3, r = 32 * q + lane;     // TMEM lane: token row
     const int turn = warp < 16 ? 0 : 1;
     if constexpr (kState) {
-      for (int ch = turn; ch < chunks; ch += 2) {
-        const int ph = (ch >> 1) & 1;
-        const bool ok = wait(sh.bars.full[turn], ph);
+      for (int ch = 0; ch < chunks; ++ch) {
+        const bool ok = wait(sh.bars.full[ch & 1], (ch >> 1) & 1);
         float f;
-        if (ok) clean_v(ch, r);
-        if (!find_exp(ch, r, 3 + turn, ok, &f)) break;
-        decay_k(ch, r, f, true);
-        arrive(sh.bars.k[turn]);
+        if (!find_exp(ch, r, turn, 3, ok, &f)) break;
+        decay_k(ch, r, turn, f, true);
+        arrive(sh.bars.k[ch & 1]);
       }
     } else {
       const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
@@ -686,9 +695,9 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         // The row's power of two, from a bound on its scores, 128 max|q_i| max|k|: a few bits more
         // than they have, of the 29 between fp16's largest and smallest normal values.
         if (!wait(sh.bars.full[turn], ph)) break;
-        const float top_q = row_top(tile_q(turn), r);
+        const float top_q = row_top(row_at(tile_q(turn), r));
         if (!wait(sh.bars.v[turn], ph)) break;
-        const int e = up_to_half(top_q * max4(sh.top_k[turn]) * (128.0f * fabsf(w.a)));
+        const int e = up_to_half(top_q * max8(sh.top_k[turn]) * (128.0f * fabsf(w.a)));
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         const bool bad_k = bad || tokens(ch) < kC;   // rows past the end may hold anything
         if (!wait(sh.bars.scores[turn], ph)) break;
@@ -745,7 +754,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         __half* row = op + (row0(ch) + r) * w.o_t;
 #pragma unroll 1
         for (int b = 0; b < 8; ++b) {
-          uint32_t x[32], y[32];
+          uint32_t x[32], y[32];   // sixteen of each
           tc_ld_32x32b_x16(t_qs + lane_addr + 16u * b, x);
           tc_ld_32x32b_x16(t_pv + lane_addr + 16u * b, y);
           tc_wait_ld();
@@ -755,8 +764,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
           }
           uint32_t u[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-          {
+          for (int j = 0; j < 8; ++j) {
             const float2 o = unpair(
                 fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fi2,
                      mul2(pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), fa2)));

@@ -45,6 +45,7 @@
 #include <mutex>
 
 #include "backward.cuh"
+#include "int8_linear.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -60,9 +61,14 @@ constexpr int kThreads = 192;
 constexpr int kOutBuf = kRows * 128;       // 128 rows x 128 bytes (64 fp16 / 32 fp32 columns)
 constexpr int kBarBytes = 256;
 constexpr int kSmem = 1024 + kS * kStage + 2 * kOutBuf + kBarBytes;
+constexpr int kScaleBytes = 2 * kRows * 4; // channel scales of a tile (kI8Channel)
 constexpr uint64_t kDrainNs = 2000000000ull;
 static_assert(8 * (2 * kS + 5) <= kBarBytes, "barrier area");
-static_assert(kSmem <= 227 * 1024, "shared memory per block");
+static_assert(kSmem + kScaleBytes + 16 <= 227 * 1024, "shared memory per block");
+
+// What the operands are and how the sums become outputs: ternary codes with one scale for the
+// matrix, fp16 with one scale, or int8 codes with a scale for each channel (weight row).
+enum Kind { kI8Ternary, kF16Kind, kI8Channel };
 
 struct SParams {
   int64_t T;         // rows of A (tokens; for the weight gradient, output rows)
@@ -77,6 +83,7 @@ struct SParams {
   int n_tiles;
   const float* gamma;
   const float* beta;
+  const float* wscale;   // kI8Channel: [rows]
   unsigned* status;
   uint64_t wait_limit_ns;
 };
@@ -133,10 +140,11 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kF16>
+template <Kind kKind>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_y, const SParams p) {
+  constexpr bool kF16 = kKind == kF16Kind;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -144,6 +152,7 @@ prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
   uint8_t* s_b = s_a + kS * kOpStage;         // kS x 16 KB, weight codes (B)
   uint8_t* s_out = s_b + kS * kOpStage;       // 2 x 16 KB output tiles
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_out + 2 * kOutBuf);
+  float* s_ws = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -299,7 +308,7 @@ prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const bool to_i32 = p.out_mode == kOutI32;
     const bool to_f16 = p.out_mode == kOutF16;
-    const float beta = to_i32 ? 0.0f : (p.beta ? *p.beta : 1.0f);
+    const float beta = to_i32 || kKind == kI8Channel ? 0.0f : (p.beta ? *p.beta : 1.0f);
     const uint32_t accempty0[2] = {map_peer(accempty(0), 0), map_peer(accempty(1), 0)};
     int nbuf = 0;                                      // output tiles used so far (alternating)
     int last_buf = -1;                                 // tile of the newest committed store
@@ -314,9 +323,20 @@ prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
       float sc;
       if constexpr (kF16)
         sc = beta;
+      else if constexpr (kKind == kI8Channel)
+        sc = t < p.T ? __fdiv_rn(p.gamma[t], 127.0f) : 0.0f;
       else
         sc = (!to_i32 && t < p.T) ? __fmul_rn(__fdiv_rn(p.gamma[t], 127.0f), beta) : 0.0f;
       const int b = n & 1;
+      if constexpr (kKind == kI8Channel) {
+        // the tile's channel scales: every read of the last tile's came before a barrier of its
+        // last column block, and the barrier below publishes these
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int row = wt * 2 * kRows + z * kRows + et;
+          s_ws[z * kRows + et] = row < p.ncols ? p.wscale[row] : 0.0f;
+        }
+      }
       const bool w = mbar_wait_bounded_cluster(accfull(b), (n >> 1) & 1, p.wait_limit_ns,
                                                abort_flag, p.status);
       if (!named_bar_and(1, 128, __all_sync(0xFFFFFFFFu, w))) break;
@@ -331,17 +351,26 @@ prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         // this block's values, as 32-bit words in output order
         uint32_t o[32];
         const int c0 = cb * cols_per_buf;
-        if (!p.glu) {
+        if (kKind == kI8Channel || !p.glu) {
           uint32_t v[32];
           if (to_f16) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               tc_ld_32x32b_x32(dcol + static_cast<uint32_t>(c0 + 32 * hh), v);
               tc_wait_ld();
+              if constexpr (kKind == kI8Channel) {
+                const float* ws = s_ws + c0 + 32 * hh;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                o[16 * hh + j] = pack_half2(static_cast<float>(static_cast<int32_t>(v[2 * j])) * sc,
-                                            static_cast<float>(static_cast<int32_t>(v[2 * j + 1])) * sc);
+                for (int j = 0; j < 16; ++j)
+                  o[16 * hh + j] =
+                      pack_half2(static_cast<float>(static_cast<int32_t>(v[2 * j])) * (sc * ws[2 * j]),
+                                 static_cast<float>(static_cast<int32_t>(v[2 * j + 1])) * (sc * ws[2 * j + 1]));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  o[16 * hh + j] = pack_half2(static_cast<float>(static_cast<int32_t>(v[2 * j])) * sc,
+                                              static_cast<float>(static_cast<int32_t>(v[2 * j + 1])) * sc);
+              }
             }
           } else {
             tc_ld_32x32b_x32(dcol + static_cast<uint32_t>(c0), v);
@@ -350,6 +379,8 @@ prefill_ss_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             for (int j = 0; j < 32; ++j) {
               if constexpr (kF16)
                 o[j] = __float_as_uint(__uint_as_float(v[j]) * sc);
+              else if constexpr (kKind == kI8Channel)
+                o[j] = __float_as_uint(static_cast<float>(static_cast<int32_t>(v[j])) * (sc * s_ws[c0 + j]));
               else
                 o[j] = to_i32 ? v[j]
                               : __float_as_uint(static_cast<float>(static_cast<int32_t>(v[j])) * sc);
@@ -456,8 +487,11 @@ bool prefill_ss_supported(const GemmCall& c) { return c.T > 128 && c.rows % 256 
 
 namespace {
 
+template <Kind kKind>
+constexpr int smem_of() { return kSmem + (kKind == kI8Channel ? kScaleBytes : 0); }
+
 // CTA pairs of the pair kernel that fit on the device at once (per device and operand kind).
-template <bool kF16>
+template <Kind kKind>
 cudaError_t pair_setup(int* pairs_out, int* sms_out) {
   static std::once_flag once[kMaxDevices];
   static int pairs[kMaxDevices], sms[kMaxDevices];
@@ -467,15 +501,15 @@ cudaError_t pair_setup(int* pairs_out, int* sms_out) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [&] {
-    cudaError_t ae = cudaFuncSetAttribute(prefill_ss_kernel<kF16>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t ae = cudaFuncSetAttribute(prefill_ss_kernel<kKind>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<kKind>());
     if (ae == cudaSuccess) ae = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
     int nc = 0;
     if (ae == cudaSuccess) {
       cudaLaunchConfig_t q = {};
       q.gridDim = dim3(2 * static_cast<unsigned>(sms[dev] / 2));
       q.blockDim = dim3(kThreads);
-      q.dynamicSmemBytes = kSmem;
+      q.dynamicSmemBytes = smem_of<kKind>();
       cudaLaunchAttribute ca;
       ca.id = cudaLaunchAttributeClusterDimension;
       ca.val.clusterDim.x = 2;
@@ -483,7 +517,7 @@ cudaError_t pair_setup(int* pairs_out, int* sms_out) {
       ca.val.clusterDim.z = 1;
       q.attrs = &ca;
       q.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&nc, prefill_ss_kernel<kF16>, &q) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&nc, prefill_ss_kernel<kKind>, &q) != cudaSuccess) {
         (void)cudaGetLastError();
         nc = 0;
       }
@@ -498,7 +532,7 @@ cudaError_t pair_setup(int* pairs_out, int* sms_out) {
   return cudaSuccess;
 }
 
-template <bool kF16>
+template <Kind kKind>
 cudaError_t launch_pairs(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_y,
                          const SParams& p, int pairs, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(p.n_tiles) * p.ksplit;
@@ -506,7 +540,7 @@ cudaError_t launch_pairs(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * np));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem_of<kKind>();
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -517,7 +551,7 @@ cudaError_t launch_pairs(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, prefill_ss_kernel<kF16>, tm_a, tm_b, tm_y, p);
+  return cudaLaunchKernelEx(&cfg, prefill_ss_kernel<kKind>, tm_a, tm_b, tm_y, p);
 }
 
 // y[m][n] = sum over the splits of part[split][m][n], for m < M (float4 at a time).
@@ -544,7 +578,7 @@ constexpr int kNominalPairs = 74;   // split choice for a 148-SM part, independe
 
 cudaError_t launch_prefill_ss(const GemmCall& c, int8_t* w8, cudaStream_t s) {
   int pairs = 0, sms = 0;
-  cudaError_t e = pair_setup<false>(&pairs, &sms);
+  cudaError_t e = pair_setup<kI8Ternary>(&pairs, &sms);
   if (e != cudaSuccess) return e;
 
   // 1. expand the packed codes into int8 codes (N x K bytes)
@@ -590,9 +624,49 @@ cudaError_t launch_prefill_ss(const GemmCall& c, int8_t* w8, cudaStream_t s) {
   p.n_tiles = static_cast<int>(n_tiles);
   p.gamma = c.gamma;
   p.beta = c.beta;
+  p.wscale = nullptr;
   p.status = c.status;
   p.wait_limit_ns = c.wait_limit_ns;
-  return launch_pairs<false>(tm_a, tm_b, tm_y, p, pairs, s);
+  return launch_pairs<kI8Ternary>(tm_a, tm_b, tm_y, p, pairs, s);
+}
+
+// The 8-bit projection with the codes as they are: columns past K and rows past N read as zeros,
+// outputs past N or T are not stored.
+cudaError_t launch_int8_pairs(const Int8Call& c, cudaStream_t s) {
+  int pairs = 0, sms = 0;
+  cudaError_t e = pair_setup<kI8Channel>(&pairs, &sms);
+  if (e != cudaSuccess) return e;
+  const uint64_t K = static_cast<uint64_t>(c.K);
+  const bool f16 = c.out_mode == kOutF16;
+  CUtensorMap tm_a, tm_b, tm_y;
+  if (!make_tmap_2d_u8(&tm_a, c.A, K, static_cast<uint64_t>(c.T), K, kKB, kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d_u8(&tm_b, c.W8, K, static_cast<uint64_t>(c.N), K, kKB, kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tm_y, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                    c.y, static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.T),
+                    static_cast<uint64_t>(c.N) * (f16 ? 2 : 4), f16 ? 64 : 32, kRows,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  SParams p;
+  p.T = c.T;
+  p.nkb = (c.K + kKB - 1) / kKB;
+  p.ksplit = 1;
+  p.slab = 0;
+  p.ncols = c.N;
+  p.glu = 0;
+  p.half = 0;
+  p.out_mode = c.out_mode;
+  p.n_wt = (c.N + 2 * kRows - 1) / (2 * kRows);
+  const int64_t n_tiles = (c.T + 2 * kRows - 1) / (2 * kRows) * p.n_wt;
+  if (n_tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  p.n_tiles = static_cast<int>(n_tiles);
+  p.gamma = c.gamma;
+  p.beta = nullptr;
+  p.wscale = c.wscale;
+  p.status = c.status;
+  p.wait_limit_ns = c.wait_limit_ns;
+  return launch_pairs<kI8Channel>(tm_a, tm_b, tm_y, p, pairs, s);
 }
 
 int f16_gemm_split(int64_t M, int rows, int64_t Kc) {
@@ -625,7 +699,7 @@ size_t f16_gemm_part_bytes(int64_t M, int rows, int ksplit) {
 
 cudaError_t launch_f16_gemm(const F16GemmCall& c, cudaStream_t s) {
   int pairs = 0, sms = 0;
-  cudaError_t e = pair_setup<true>(&pairs, &sms);
+  cudaError_t e = pair_setup<kF16Kind>(&pairs, &sms);
   if (e != cudaSuccess) return e;
   const int ks = c.ksplit < 1 ? 1 : c.ksplit;
   const int64_t slab = (c.M + 255) / 256 * 256;
@@ -663,9 +737,10 @@ cudaError_t launch_f16_gemm(const F16GemmCall& c, cudaStream_t s) {
   p.n_tiles = static_cast<int>(n_tiles);
   p.gamma = nullptr;
   p.beta = c.scale;
+  p.wscale = nullptr;
   p.status = c.status;
   p.wait_limit_ns = c.wait_limit_ns;
-  e = launch_pairs<true>(tm_a, tm_b, tm_y, p, pairs, s);
+  e = launch_pairs<kF16Kind>(tm_a, tm_b, tm_y, p, pairs, s);
   if (e != cudaSuccess || ks == 1) return e;
   const int64_t n_vec = c.M * c.rows / 4;
   const int64_t want = (n_vec + 255) / 256;
