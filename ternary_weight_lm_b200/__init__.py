@@ -472,45 +472,49 @@ def bitlinear_backward(x, Wp, beta, dy, norm_w=None, eps=1e-8, A=None, gamma=Non
 
 # ------------------------------------------------------------- 8-bit projection, linear attention
 def _tensor(name, t, shape, dtypes, device, contiguous=True):
-    """Refuses a tensor that the call would misread."""
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    """Refuses a tensor that the call would misread: dtypes a tuple, shape with None for any."""
+    got = t.shape
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if got != shape and (len(got) != len(shape) or
+                         any(s is not None and s != n for s, n in zip(shape, got))):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {shape}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif got[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 class _On:
     """Makes a tensor's device and the call's stream current, so that what the call allocates
     belongs to the stream that uses it; ``handle`` is the stream's."""
+    __slots__ = ("device", "given", "stream", "handle")
 
     def __init__(self, t, stream):
         import torch
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"tensors must be on a GPU, got {t.device}")
+        at = t.get_device()
         self.device = self.stream = None
-        if t.device.index != torch.cuda.current_device():
-            self.device = torch.cuda.device(t.device)
-        if isinstance(stream, int):
+        if at != torch._C._cuda_getDevice():
+            self.device = torch.cuda.device(at)
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(at)
+        elif isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=t.device)
         self.given = stream
 
     def __enter__(self):
-        import torch
         if self.device is not None:
             self.device.__enter__()
         if self.given is not None:
+            import torch
             self.stream = torch.cuda.stream(self.given)
             self.stream.__enter__()
             self.handle = self.given.cuda_stream
-        else:
-            self.handle = torch.cuda.current_stream().cuda_stream
         return self
 
     def __exit__(self, *exc):
@@ -535,12 +539,12 @@ def int8_matmul(A, gamma, W8, wscale, out_dtype=None, out=None, stream=None):
     """y [T, N] of activation codes A [T, K] with scales gamma [T] (mmf_quantize_activations) and
     weights from quantize_weights_int8; fp16 unless out_dtype or out says otherwise."""
     import torch
-    _tensor("A", A, (None, None), torch.int8, A.device)
+    _tensor("A", A, (None, None), (torch.int8,), A.device)
     T, K = A.shape
-    _tensor("W8", W8, (None, K), torch.int8, A.device)
+    _tensor("W8", W8, (None, K), (torch.int8,), A.device)
     N = W8.shape[0]
-    _tensor("gamma", gamma, (T,), torch.float32, A.device)
-    _tensor("wscale", wscale, (N,), torch.float32, A.device)
+    _tensor("gamma", gamma, (T,), (torch.float32,), A.device)
+    _tensor("wscale", wscale, (N,), (torch.float32,), A.device)
     if out is not None:
         _tensor("out", out, (T, N), (torch.float32, torch.float16), A.device)
     with _On(A, stream) as on:
@@ -557,11 +561,11 @@ def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws
     f = (torch.float32, torch.float16)
     _tensor("x", x, (None, None), f, x.device)
     T, K = x.shape
-    _tensor("W8", W8, (None, K), torch.int8, x.device)
+    _tensor("W8", W8, (None, K), (torch.int8,), x.device)
     N = W8.shape[0]
-    _tensor("wscale", wscale, (N,), torch.float32, x.device)
+    _tensor("wscale", wscale, (N,), (torch.float32,), x.device)
     if norm_w is not None:
-        _tensor("norm_w", norm_w, (K,), torch.float32, x.device)
+        _tensor("norm_w", norm_w, (K,), (torch.float32,), x.device)
     with _On(x, stream) as on:
         y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
         if ws is None:
@@ -576,25 +580,21 @@ def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
     dev, f = q.device, (torch.float32, torch.float16)
     _tensor("q", q, (None, None, None), f, dev, contiguous=False)
     T, H, dk = q.shape
-    _tensor("k", k, (T, H, dk), q.dtype, dev, contiguous=False)
-    _tensor("v", v, (T, H, None), q.dtype, dev, contiguous=False)
+    _tensor("k", k, (T, H, dk), (q.dtype,), dev, contiguous=False)
+    _tensor("v", v, (T, H, None), (q.dtype,), dev, contiguous=False)
     dv = v.shape[2]
-    _tensor("log_decay", log_decay, (H,), torch.float32, dev)
+    _tensor("log_decay", log_decay, (H,), (torch.float32,), dev)
     if o is not None:
-        _tensor("out", o, (T, H, dv), q.dtype, dev, contiguous=False)
+        _tensor("out", o, (T, H, dv), (q.dtype,), dev, contiguous=False)
     if cu_seqlens is not None:
-        _tensor("cu_seqlens", cu_seqlens, (None,), torch.int32, dev)
+        _tensor("cu_seqlens", cu_seqlens, (None,), (torch.int32,), dev)
         if batch is not None and batch != cu_seqlens.numel() - 1:
             raise ValueError(f"batch {batch}, but cu_seqlens has {cu_seqlens.numel() - 1} sequences")
         batch = cu_seqlens.numel() - 1
-    d = LinattnDesc()
-    d.T, d.B, d.H, d.dk, d.dv = T, 1 if batch is None else batch, H, dk, dv
-    d.cu_seqlens, d.dt, d.log_decay = _ptr(cu_seqlens), _dt(q), _ptr(log_decay)
-    d.scale = dk ** -0.5 if scale is None else scale
-    d.q_t, d.q_h, d.k_t, d.k_h = q.stride(0), q.stride(1), k.stride(0), k.stride(1)
-    d.v_t, d.v_h = v.stride(0), v.stride(1)
-    d.o_t, d.o_h = (H * dv, dv) if o is None else (o.stride(0), o.stride(1))
-    return d
+    return LinattnDesc(
+        T, 1 if batch is None else batch, _ptr(cu_seqlens), H, dk, dv, _dt(q),
+        dk ** -0.5 if scale is None else scale, _ptr(log_decay), *q.stride()[:2],
+        *k.stride()[:2], *v.stride()[:2], *((H * dv, dv) if o is None else o.stride()[:2]))
 
 
 def _linattn_ws(ws, need, device):
@@ -615,7 +615,7 @@ def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None,
     state = (d.B, d.H, d.dk, d.dv)
     for name, t in (("h0", h0), ("hT", hT)):
         if t is not None:
-            _tensor(name, t, state, torch.float32, q.device)
+            _tensor(name, t, state, (torch.float32,), q.device)
     with _On(q, stream) as on:
         if out is None:
             out = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
@@ -631,10 +631,10 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, st
     [n, H, dk, dv] and slots names each row's state (negative: padding, zeros out)."""
     import torch
     d = _linattn(q, k, v, log_decay, out, scale, None, q.shape[0])
-    _tensor("state", state, (None if slots is not None else d.B, d.H, d.dk, d.dv), torch.float32,
+    _tensor("state", state, (None if slots is not None else d.B, d.H, d.dk, d.dv), (torch.float32,),
             q.device)
     if slots is not None:
-        _tensor("slots", slots, (d.B,), torch.int32, q.device)
+        _tensor("slots", slots, (d.B,), (torch.int32,), q.device)
     with _On(q, stream) as on:
         if out is None:
             out = torch.empty((d.B, d.H, d.dv), dtype=q.dtype, device=q.device)
@@ -653,7 +653,7 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batc
     state = (d.B, d.H, d.dk, d.dv)
     for name, t in (("h0", h0), ("dhT", dhT)):
         if t is not None:
-            _tensor(name, t, state, torch.float32, q.device)
+            _tensor(name, t, state, (torch.float32,), q.device)
     with _On(q, stream) as on:
         dq, dk = (torch.empty((d.T, d.H, d.dk), dtype=q.dtype, device=q.device) for _ in range(2))
         dv = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
