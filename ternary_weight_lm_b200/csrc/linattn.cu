@@ -380,26 +380,29 @@ size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv) {
 
 void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split) {
-  // Segments that run at once on 148 SMs: one block for a head on an SM with tcgen05, two to four
-  // on it otherwise (by the registers of a state).  A block per segment, head, sweep and tile of
-  // columns; segments are whole chunks and at least 256 tokens, below which reading k and v twice
-  // and passing states through memory costs more than the blocks that it adds.
-  constexpr int64_t kMin = 256;
+  // The kernel that these sizes take: tokens it handles at a time, blocks that run at once on 148
+  // SMs, and blocks for each segment, head and sweep.
   const bool half = dt == kInF16;
   const bool tc = half && dk == 128 && dv == 128;
-  const int64_t slots = 148 * (tc ? 1 : half && std::min(dk, dv) <= 64 ? 4 : 2);
-  const int64_t width = tc ? 1 : std::max(1, dv / (half ? 128 : 64));
-  const int64_t units = std::max<int64_t>(1, H * n_sweeps * width);
-  const int64_t longest = ragged ? T : T / B;
-  // segments of all sequences together, at most one wave of blocks
-  const int64_t all = std::max<int64_t>(1, slots / units);
-  const int64_t per = ragged ? all : std::max<int64_t>(1, all / B);
-  int64_t L = (longest + per - 1) / per;
-  L = std::max(kMin, (L + 127) / 128 * 128);
-  *split = longest > L;
-  if (!*split) L = std::max<int64_t>(longest, 1);
-  *seg_len = L;
-  *n_items = !*split ? B : ragged ? T / L + B : B * ((longest + L - 1) / L);
+  const bool mma = half && !tc && (dk == 64 || dk == 128) && dv % 64 == 0;
+  const int64_t step = tc ? 128 : mma ? 64 : 16;
+  const int64_t slots = 148 * (tc ? 1 : mma ? (dk == 128 ? 2 : dv % 128 == 0 ? 3 : 4) : 5);
+  const int64_t width = tc ? 1 : mma ? dv / (dv % 128 == 0 ? 128 : 64) : (std::max(dk, dv) + 31) / 32;
+  const int64_t room = std::max<int64_t>(1, slots / (H * n_sweeps * width));   // segments
+  // Segments that fill one wave of blocks, but of at least four steps (two of 128): below that
+  // reading k and v twice and passing states through memory costs more than the blocks add.  Of
+  // a ragged batch the host knows the sum of the lengths alone: it takes half a segment more for
+  // each sequence, and the longest for three times the mean.
+  const int64_t mean = (T + B - 1) / B;
+  const int64_t longest = ragged ? std::min(T, 3 * mean) : mean;
+  const int64_t each = ragged ? T / std::max<int64_t>(1, room - B / 2) + 1
+                              : (mean + std::max<int64_t>(1, room / B) - 1) / std::max<int64_t>(1, room / B);
+  const int64_t L = (std::max(each, (tc ? 2 : 4) * step) + step - 1) / step * step;
+  // A step over k and v alone takes about half of a whole one; two more launches about as long as
+  // three steps (8 us against 2.5 to 4).
+  *split = longest > L && (3 * L) / (2 * step) + 3 < longest / step;
+  *seg_len = *split ? L : std::max<int64_t>(ragged ? T : mean, 1);
+  *n_items = !*split ? B : ragged ? T / L + B : B * ((mean + L - 1) / L);
 }
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s) {

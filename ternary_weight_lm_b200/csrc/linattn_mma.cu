@@ -69,9 +69,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // The power of two that brings a magnitude (as the bits of a float) to 2^14 .. 2^15, as an exponent.
@@ -307,16 +304,16 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         uint32_t b[NV / 2][4];
-        bool odd = false;
+        __half2 sum = __float2half2_rn(0.0f);   // 0 times what is not finite is NaN
 #pragma unroll
         for (int v = 0; v < NV / 2; ++v) {
           ldsm4t(b[v], tile_at<DV / 8>(tile_v(s), 16 * kk + lr + 8 * (lm & 1),
                                        warp * (RV / 8) + 2 * v + (lm >> 1)));
 #pragma unroll
           for (int z = 0; z < 4; ++z)
-            odd |= (b[v][z] & 0x7c00u) == 0x7c00u || (b[v][z] & 0x7c000000u) == 0x7c000000u;
+            sum = __hfma2(*reinterpret_cast<const __half2*>(&b[v][z]), __float2half2_rn(0.0f), sum);
         }
-        odd = __any_sync(0xffffffffu, odd);
+        const bool odd = __any_sync(0xffffffffu, !__hbeq2(sum, __float2half2_rn(0.0f)));
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           if (m < kk) continue;
@@ -369,7 +366,6 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 
     // ---- the state's update
     uint32_t hi[4][MT][4], lo[4][MT][4];
-    uint32_t vtop = 0u;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -377,23 +373,29 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
         // rows of S^T (columns of v) in the low bit of the matrix, tokens in the high one
         ldsm4t(hi[kk][m], tile_at<DV / 8>(tile_v(s), 16 * kk + lr + 8 * (lm >> 1),
                                           warp * (RV / 8) + 2 * m + (lm & 1)));
+    // Their decay, in fp16 pairs of tokens: with a factor w 2^e = wh + wl, hi = v wh rounded and lo
+    // the rest (v wh - hi, exact, plus v wl), an error of about 2^-22.  e brings the warp's largest
+    // product to 2^14 .. 2^15, or the largest factor of a token that is not zero if that is less.
     auto weight = [&](int j) { return w.a * s_pow[max(n - 1 - j + lag, 0)]; };   // v is 0 past n
+    float vtop = 0.0f, wide = 0.0f;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
-        const int j = 16 * kk + 2 * t4 + 8 * z;
-        const float w0 = weight(j), w1 = weight(j + 1);
+        __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float2 x = unpack2(hi[kk][m][2 * z + y]);
-            vtop = max(vtop, max(magnitude(x.x * w0), magnitude(x.y * w1)));
-          }
+          for (int y = 0; y < 2; ++y)
+            m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __half2*>(&hi[kk][m][2 * z + y])));
+        const float2 x = __half22float2(m2);
+        const int j = 16 * kk + 2 * t4 + 8 * z;
+        const float w0 = fabsf(weight(j)), w1 = fabsf(weight(j + 1));
+        vtop = fmaxf(vtop, fmaxf(x.x * w0, x.y * w1));
+        wide = fmaxf(wide, fmaxf(x.x != 0.0f ? w0 : 0.0f, x.y != 0.0f ? w1 : 0.0f));
       }
-    vtop = __reduce_max_sync(0xffffffffu, vtop);
-    const int ev = up_to_half(vtop, 60);
+    const int ev = min(up_to_half(__reduce_max_sync(0xffffffffu, magnitude(vtop)), 60),
+                       up_to_half(__reduce_max_sync(0xffffffffu, magnitude(wide)), 60));
     const float fv = pow2(ev);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
@@ -401,16 +403,20 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
       for (int z = 0; z < 2; ++z) {
         const int j = 16 * kk + 2 * t4 + 8 * z;
         const float w0 = weight(j) * fv, w1 = weight(j + 1) * fv;
+        const __half2 wh = __floats2half2_rn(w0, w1);
+        const float2 r = __half22float2(wh);
+        const __half2 wl = __floats2half2_rn(w0 - r.x, w1 - r.y);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float2 x = unpack2(hi[kk][m][2 * z + y]);
-            const float x0 = x.x * w0, x1 = x.y * w1;
-            const uint32_t u = pack2(x0, x1);
-            const float2 r = unpack2(u);
-            hi[kk][m][2 * z + y] = u;
-            if (two) lo[kk][m][2 * z + y] = pack2(x0 - r.x, x1 - r.y);
+            const __half2 v2 = *reinterpret_cast<const __half2*>(&hi[kk][m][2 * z + y]);
+            const __half2 h2 = __hmul2(v2, wh);
+            hi[kk][m][2 * z + y] = *reinterpret_cast<const uint32_t*>(&h2);
+            if (two) {
+              const __half2 l2 = __hfma2(v2, wl, __hfma2(v2, wh, __hneg2(h2)));
+              lo[kk][m][2 * z + y] = *reinterpret_cast<const uint32_t*>(&l2);
+            }
           }
       }
     const float decay = s_pow[n], back = pow2(-ev);
