@@ -25,9 +25,9 @@ namespace {
 // ------------------------------------------------------------------ token-by-token sweep
 // Block: one segment, one head, 32 columns of the state.  Thread (r, c) holds rows 4 r + 64 j ..
 // + 3 and columns 4 c .. + 3: 4 KR values in registers, in fp32 throughout (the products too).
-// Per token and state element: decay, update, product with q, three operations of the fp32 pipe,
-// which is what bounds it (148 SMs x 128 lanes); k, q and v come from shared memory as 16-byte
-// broadcasts.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
+// Per token and state element: decay, update, product with q, three fp32 operations, two rows at a
+// time (f32x2); their issue is what bounds it.  k, q and v (each v twice, as both halves of a pair)
+// come from shared memory as 16-byte broadcasts.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
 // through shared memory once every kTok tokens.
 constexpr int kSweepThreads = 128;
 constexpr int kTok = 16;
@@ -51,14 +51,14 @@ __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__half* p, float v) { *p = __float2half_rn(v); }
 
 template <typename T, int KR, bool kState>
-__global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_constant__ LinCall c) {
+__global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 4) lin_sweep_kernel(const __grid_constant__ LinCall c) {
   constexpr int kRows = 16 * KR;           // padded dk
   constexpr int kVecRow = kRows / 4;       // 4-value vectors of a k or q row
   constexpr int kLoads = kTok * kVecRow / kSweepThreads;   // of k (and of q) per thread
   static_assert(kTok * (kCols / 4) == kSweepThreads, "one v vector per thread");
   __shared__ __align__(16) float s_k[kTok][kRows];
   __shared__ __align__(16) float s_q[kState ? 1 : kTok][kState ? 4 : kRows];
-  __shared__ __align__(16) float s_v[kTok][kCols];
+  __shared__ __align__(16) float s_v[kTok][2 * kCols];
   __shared__ float s_o[kState ? 1 : 4][kState ? 1 : kTok][kCols];
 
   const int slices = (max(c.sw[0].dv, c.sw[0].dk) + kCols - 1) / kCols;
@@ -76,20 +76,24 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
 
   // the state before the first token: the split's start state [dk x dv], or s0
-  float S[KR][4];
+  uint64_t S[KR / 2][4];   // pairs of rows
+  auto row_of = [&](int i) { return 4 * rg + (i & 3) + 64 * (i >> 2); };
 #pragma unroll
-  for (int i = 0; i < KR; ++i)
+  for (int i = 0; i < KR; i += 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = 4 * rg + (i & 3) + 64 * (i >> 2), col = col0 + 4 * cg + j;
-      float x = 0.0f;
-      if (!kState && row < w.dk && col < w.dv) {
-        if (c.split && !whole)
-          x = seg[static_cast<size_t>(row) * w.dv + col];
-        else if (w.s0)
-          x = w.s0[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val];
+      float x[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int row = row_of(i + z), col = col0 + 4 * cg + j;
+        if (!kState && row < w.dk && col < w.dv) {
+          if (c.split && !whole)
+            x[z] = seg[static_cast<size_t>(row) * w.dv + col];
+          else if (w.s0)
+            x[z] = w.s0[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val];
+        }
       }
-      S[i][j] = x;
+      S[i / 2][j] = pair(x[0], x[1]);
     }
 
   const T* kp = static_cast<const T*>(w.k) + h * w.k_h;
@@ -122,39 +126,41 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
       *reinterpret_cast<float4*>(&s_k[tok][d]) = rk[i];
       if constexpr (!kState) *reinterpret_cast<float4*>(&s_q[tok][d]) = rq[i];
     }
-    *reinterpret_cast<float4*>(&s_v[tid / (kCols / 4)][(tid % (kCols / 4)) * 4]) =
-        make_float4(rv.x * w.a, rv.y * w.a, rv.z * w.a, rv.w * w.a);
+    float4* v2 = reinterpret_cast<float4*>(&s_v[tid / (kCols / 4)][(tid % (kCols / 4)) * 8]);
+    v2[0] = make_float4(rv.x * w.a, rv.x * w.a, rv.y * w.a, rv.y * w.a);
+    v2[1] = make_float4(rv.z * w.a, rv.z * w.a, rv.w * w.a, rv.w * w.a);
     __syncthreads();
     if (p0 + kTok < g.n) fetch(p0 + kTok);
     const int nt = static_cast<int>(min(static_cast<int64_t>(kTok), g.n - p0));
     for (int tok = 0; tok < nt; ++tok) {
-      const float4 v4 = *reinterpret_cast<const float4*>(&s_v[tok][4 * cg]);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const ulonglong2 va = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg]);
+      const ulonglong2 vb = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg + 4]);
+      const uint64_t v2[4] = {va.x, va.y, vb.x, vb.y}, dec2 = pair(dec, dec);
+      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // of the even and of the odd rows
 #pragma unroll
       for (int i4 = 0; i4 < KR / 4; ++i4) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&s_k[tok][4 * rg + 64 * i4]);
-        const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
-        float qq[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (!kState) {
-          const float4 q4 = *reinterpret_cast<const float4*>(&s_q[tok][4 * rg + 64 * i4]);
-          qq[0] = q4.x; qq[1] = q4.y; qq[2] = q4.z; qq[3] = q4.w;
-        }
+        const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(&s_k[tok][4 * rg + 64 * i4]);
+        ulonglong2 q4 = make_ulonglong2(0ull, 0ull);
+        if constexpr (!kState) q4 = *reinterpret_cast<const ulonglong2*>(&s_q[tok][4 * rg + 64 * i4]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float* Sr = S[4 * i4 + i];
-          Sr[0] = fmaf(kk[i], v4.x, dec * Sr[0]);
-          Sr[1] = fmaf(kk[i], v4.y, dec * Sr[1]);
-          Sr[2] = fmaf(kk[i], v4.z, dec * Sr[2]);
-          Sr[3] = fmaf(kk[i], v4.w, dec * Sr[3]);
-          if constexpr (!kState) {
+        for (int z = 0; z < 2; ++z) {
+          uint64_t* Sr = S[2 * i4 + z];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = fmaf(qq[i], Sr[j], acc[j]);
+          for (int j = 0; j < 4; ++j) {
+            Sr[j] = fma2(z ? k4.y : k4.x, v2[j], mul2(dec2, Sr[j]));
+            if constexpr (!kState) sum[j] = fma2(z ? q4.y : q4.x, Sr[j], sum[j]);
           }
         }
       }
       dec = gamma.next();
       if constexpr (!kState) {
         // sum over the warp's four row groups (lane bits 3 and 4); each lane ends with a column
+        float acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpair(sum[j]);
+          acc[j] = x.x + x.y;
+        }
         const bool hi16 = tid & 16, hi8 = tid & 8;
         float a0 = hi16 ? acc[2] : acc[0], a1 = hi16 ? acc[3] : acc[1];
         const float b0 = hi16 ? acc[0] : acc[2], b1 = hi16 ? acc[1] : acc[3];
@@ -185,13 +191,14 @@ __global__ void __launch_bounds__(kSweepThreads) lin_sweep_kernel(const __grid_c
   for (int i = 0; i < KR; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = 4 * rg + (i & 3) + 64 * (i >> 2), col = col0 + 4 * cg + j;
+      const int row = row_of(i), col = col0 + 4 * cg + j;
       if (row >= w.dk || col >= w.dv) continue;
+      const float2 p = unpair(S[i / 2][j]);
+      const float x = ((i & 1) ? p.y : p.x) * end;
       if (kState)
-        seg[static_cast<size_t>(row) * w.dv + col] = S[i][j] * end;
+        seg[static_cast<size_t>(row) * w.dv + col] = x;
       else
-        w.sT[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val] =
-            S[i][j] * end;
+        w.sT[state0 + static_cast<size_t>(row) * w.s_key + static_cast<size_t>(col) * w.s_val] = x;
     }
 }
 
@@ -386,7 +393,8 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
   const bool tc = half && dk == 128 && dv == 128;
   const bool mma = half && !tc && (dk == 64 || dk == 128) && dv % 64 == 0;
   const int64_t step = tc ? 128 : mma ? 64 : 16;
-  const int64_t slots = 148 * (tc ? 1 : mma ? (dk == 128 ? 2 : dv % 128 == 0 ? 3 : 4) : 5);
+  const int64_t slots = 148 * (tc ? 1 : mma ? (dk == 128 ? 2 : dv % 128 == 0 ? 3 : 4)
+                                          : std::max(dk, dv) > 128 ? 2 : 4);
   const int64_t width = tc ? 1 : mma ? dv / (dv % 128 == 0 ? 128 : 64) : (std::max(dk, dv) + 31) / 32;
   const int64_t room = std::max<int64_t>(1, slots / (H * n_sweeps * width));   // segments
   // Segments that fill one wave of blocks, but of at least four steps (two of 128): below that
