@@ -20,10 +20,11 @@ namespace mmf {
 namespace {
 
 // ------------------------------------------------------------------------------- weights
-// One row per block.  Up to kHeld vectors of eight values a thread stay in registers between the
-// maximum and the encoding (rows of up to 4096); longer rows are read again, from L2.
+// A block takes kHeld / V rows at a time, a thread V vectors of eight values of each, held in
+// registers between the maximum and the encoding: 32 to 64 KB in flight whatever the row's length.
+// Rows of more than 4096 values are taken one at a time, beyond kHeld vectors read again (from L2).
 constexpr int kQThreads = 128;
-constexpr int kHeld = 4;
+constexpr int kHeld = 8;
 
 struct Vec8 {
   float v[8];
@@ -33,13 +34,13 @@ template <typename TW>
 __device__ __forceinline__ Vec8 load8(const TW* p);
 template <>
 __device__ __forceinline__ Vec8 load8<float>(const float* p) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 template <>
 __device__ __forceinline__ Vec8 load8<__half>(const __half* p) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
   const __half2* h = reinterpret_cast<const __half2*>(&a);
   Vec8 r;
 #pragma unroll
@@ -51,59 +52,96 @@ __device__ __forceinline__ Vec8 load8<__half>(const __half* p) {
   return r;
 }
 
-// Division, not a product with the reciprocal: the code of a value next to a half must not
-// depend on how the scale's reciprocal rounds.
-__device__ __forceinline__ uint2 encode8(const Vec8& x, float s) {
-  uint32_t w[2] = {0u, 0u};
+// round(x / s).  The product with 1 / s is off by less than 2^-15 (three roundings of up to 2^-24 of
+// at most 127), so unless it lies that close to a half it rounds to the same code; next to a half
+// (about one vector in a hundred) the division itself decides.
+__device__ __forceinline__ uint2 encode8(const Vec8& x, float s, float inv) {
+  int c[8];
+  bool sure = inv <= 3.0e38f;   // not of a scale of zero, or one whose reciprocal overflows
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int c = s > 0.0f ? __float2int_rn(__fdiv_rn(x.v[i], s)) : 0;
-    c = max(-127, min(127, c));
-    w[i >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (i & 3));
+    const float y = x.v[i] * inv;
+    c[i] = __float2int_rn(y);
+    sure &= fabsf(fabsf(y - static_cast<float>(c[i])) - 0.5f) > 0x1p-14f;   // false for a NaN
   }
+  if (!sure) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = s > 0.0f ? __float2int_rn(__fdiv_rn(x.v[i], s)) : 0;
+  }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i >> 2] |= (static_cast<uint32_t>(max(-127, min(127, c[i]))) & 0xFFu) << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
 
-template <typename TW>
-__global__ void __launch_bounds__(kQThreads) quantize_rows_i8_kernel(const TW* __restrict__ W, int K,
+template <typename TW, int V>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_i8_kernel(const TW* __restrict__ W,
+                                                                     int64_t N, int K,
                                                                      int8_t* __restrict__ W8,
                                                                      float* __restrict__ wscale) {
-  __shared__ float s_max[kQThreads / 32];
-  const int64_t row = blockIdx.x;
-  const TW* w = W + row * K;
+  constexpr int R = kHeld / V;
+  __shared__ float s_max[R][kQThreads / 32];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R;
   const int nvec = K / 8;
-  Vec8 held[kHeld];
-  float m = 0.0f;
+  Vec8 held[R][V];
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int i = threadIdx.x + j * kQThreads;
-    if (i < nvec) held[j] = load8<TW>(w + static_cast<int64_t>(i) * 8);
-    else held[j] = Vec8{};
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = threadIdx.x + j * kQThreads;
+      held[r][j] = i < nvec && row0 + r < N ? load8<TW>(W + (row0 + r) * K + static_cast<int64_t>(i) * 8)
+                                            : Vec8{};
+    }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(held[r][j].v[e]));
+    if constexpr (R == 1) {
+      for (int i = threadIdx.x + V * kQThreads; i < nvec; i += kQThreads) {
+        const Vec8 x = load8<TW>(W + row0 * K + static_cast<int64_t>(i) * 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x.v[e]));
+      }
+    }
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if ((threadIdx.x & 31) == 0) s_max[r][threadIdx.x >> 5] = m;
   }
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(held[j].v[e]));
-  for (int i = threadIdx.x + kHeld * kQThreads; i < nvec; i += kQThreads) {
-    const Vec8 x = load8<TW>(w + static_cast<int64_t>(i) * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x.v[e]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  const float s = __fdiv_rn(m, 127.0f);
-  if (threadIdx.x == 0) wscale[row] = s;
-  uint2* out = reinterpret_cast<uint2*>(W8 + row * K);
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int i = threadIdx.x + j * kQThreads;
-    if (i < nvec) out[i] = encode8(held[j], s);
+  for (int r = 0; r < R; ++r) {
+    if (row0 + r >= N) break;
+    const float m = fmaxf(fmaxf(s_max[r][0], s_max[r][1]), fmaxf(s_max[r][2], s_max[r][3]));
+    const float s = __fdiv_rn(m, 127.0f), inv = __fdiv_rn(1.0f, s);
+    if (threadIdx.x == 0) wscale[row0 + r] = s;
+    uint2* out = reinterpret_cast<uint2*>(W8 + (row0 + r) * K);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = threadIdx.x + j * kQThreads;
+      if (i < nvec) out[i] = encode8(held[r][j], s, inv);
+    }
+    if constexpr (R == 1)
+      for (int i = threadIdx.x + V * kQThreads; i < nvec; i += kQThreads)
+        out[i] = encode8(load8<TW>(W + row0 * K + static_cast<int64_t>(i) * 8), s, inv);
   }
-  for (int i = threadIdx.x + kHeld * kQThreads; i < nvec; i += kQThreads)
-    out[i] = encode8(load8<TW>(w + static_cast<int64_t>(i) * 8), s);
+}
+
+template <typename TW>
+cudaError_t quantize_rows(const TW* W, int64_t N, int K, int8_t* W8, float* wscale, cudaStream_t s) {
+  const int per = (K / 8 + kQThreads - 1) / kQThreads;   // vectors a thread has of a row
+  auto blocks = [&](int rows) { return static_cast<unsigned>((N + rows - 1) / rows); };
+  if (per <= 1)
+    quantize_rows_i8_kernel<TW, 1><<<blocks(8), kQThreads, 0, s>>>(W, N, K, W8, wscale);
+  else if (per <= 2)
+    quantize_rows_i8_kernel<TW, 2><<<blocks(4), kQThreads, 0, s>>>(W, N, K, W8, wscale);
+  else if (per <= 4)
+    quantize_rows_i8_kernel<TW, 4><<<blocks(2), kQThreads, 0, s>>>(W, N, K, W8, wscale);
+  else
+    quantize_rows_i8_kernel<TW, 8><<<blocks(1), kQThreads, 0, s>>>(W, N, K, W8, wscale);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------- contraction
@@ -405,14 +443,8 @@ cudaError_t launch_bn(const Int8Call& c, cudaStream_t s) {
 
 cudaError_t launch_quantize_weights_i8(const void* W, int wdt, int64_t N, int K, int8_t* W8,
                                        float* wscale, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(N);
-  if (wdt == kInF16)
-    quantize_rows_i8_kernel<__half><<<blocks, kQThreads, 0, s>>>(static_cast<const __half*>(W), K,
-                                                                 W8, wscale);
-  else
-    quantize_rows_i8_kernel<float><<<blocks, kQThreads, 0, s>>>(static_cast<const float*>(W), K, W8,
-                                                                wscale);
-  return cudaGetLastError();
+  if (wdt == kInF16) return quantize_rows(static_cast<const __half*>(W), N, K, W8, wscale, s);
+  return quantize_rows(static_cast<const float*>(W), N, K, W8, wscale, s);
 }
 
 // Which contraction.  The CTA-pair pipeline takes 256 x 256 tiles over the whole of K (about 5 us
