@@ -16,10 +16,9 @@
 // 4-7 the state's (row = column of v; its 128 values stay in the thread's registers), 8-11 K -> K',
 // 12-15 and 16-19 the tokens' (scores and outputs), taking turns at the chunks, so that one's
 // outputs overlap the other's scores.  Registers go from the first group to the state's.
-// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' overwrites K once
-// Q K^T is done.  Where the state is an output (fp32), K' has a second fp16 part (22 bits in all),
-// which overwrites Q once Q S is done.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P
-// overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
+// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' has two fp16 parts
+// (22 bits), so that the state, an fp32 output, keeps its precision; once Q K^T and Q S are done
+// they overwrite K and Q.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
 // stay in the instruction cache.
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
@@ -415,7 +414,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     *f = wt * pow2(e);
     return true;
   };
-  auto decay_k = [&](int chunk, int r, int panel, float f, bool two) {
+  auto decay_k = [&](int chunk, int r, int panel, float f) {
     const uint32_t row = row_at(tile_k(chunk & 1) + panel * kPanel, r);
     const uint32_t row2 = row_at(tile_q(chunk & 1) + panel * kPanel, r);
     const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
@@ -438,17 +437,13 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
         for (int i = 0; i < 4; ++i) h2[i] = __hmul2(k2[i], wh);
         sts128(vec_of(row, x0 + x), hi);
-        if (two) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
-          sts128(vec_of(row2, x0 + x), lo);
-        }
+        for (int i = 0; i < 4; ++i) l2[i] = __hfma2(k2[i], wl, __hfma2(k2[i], wh, __hneg2(h2[i])));
+        sts128(vec_of(row2, x0 + x), lo);
       }
     }
     fence_proxy_async_smem();
   };
-  // the state is an output: K' in two parts
-  const bool two = kState || (whole && w.sT != nullptr);
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -509,7 +504,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), 0);
-        if (two) product_mn(t_upd, tile_v(s), tile_q(s), 1);
+        product_mn(t_upd, tile_v(s), tile_q(s), 1);
         commit(sh.bars.upd);
         ok = wait(sh.bars.p[s], ph);
         if (!ok) break;
@@ -629,7 +624,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int r = 32 * (warp & 3) + lane;
     for (int ch = 0; ch < chunks; ++ch) {
       const int s = ch & 1, ph = (ch >> 1) & 1;
-      bool ok = wait(sh.bars.full[s], ph);
+      const bool ok = wait(sh.bars.full[s], ph);
       if (ok) clean_v(ch, r);
       if constexpr (kState) {
         if (!ok) break;
@@ -638,10 +633,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         float f;
         if (!find_exp(ch, r, 0, 2, ok, &f)) break;
         arrive(sh.bars.v[s]);
-        // K, and with two parts Q, are no longer read as such
-        ok = two ? wait(sh.bars.qk, ch & 1) : wait(sh.bars.scores[s], ph);
-        if (!ok) break;
-        decay_k(ch, r, 0, f, two);
+        if (!wait(sh.bars.qk, ch & 1)) break;   // K and Q are no longer read as such
+        decay_k(ch, r, 0, f);
         arrive(sh.bars.k[s]);
       }
     }
@@ -654,7 +647,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         const bool ok = wait(sh.bars.full[ch & 1], (ch >> 1) & 1);
         float f;
         if (!find_exp(ch, r, turn, 3, ok, &f)) break;
-        decay_k(ch, r, turn, f, true);
+        decay_k(ch, r, turn, f);
         arrive(sh.bars.k[ch & 1]);
       }
     } else {
