@@ -16,9 +16,9 @@
 // 4-7 the state's (row = column of v; its 128 values stay in the thread's registers), 8-11 K -> K',
 // 12-15 and 16-19 the tokens' (scores and outputs), taking turns at the chunks, so that one's
 // outputs overlap the other's scores.  Registers go from the first group to the state's.
-// Shared memory: two stages of K, V, Q (192 KB) and the fp16 state (32 KB).  K' has two fp16 parts
-// (22 bits), so that the state, an fp32 output, keeps its precision; once Q K^T and Q S are done
-// they overwrite K and Q.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
+// K' has two fp16 parts (22 bits), so that the state, an fp32 output, keeps its precision; the first
+// overwrites K once Q K^T is done.  Shared memory, 32 KB each: two stages of K and V, the second
+// part of K', Q (loaded again as soon as Q S is done), the fp16 state.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
 // stay in the instruction cache.
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
@@ -60,9 +60,12 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 template <bool kState>
 struct Lay {
   static constexpr int kStages = 2;
-  static constexpr int kStage = 3 * kTile;   // K, V, Q (kState: room for the second part of K')
-  static constexpr int kS = kStages * kStage;
-  static constexpr int kSmem = 1024 + kS + (kState ? 0 : kTile);
+  // kState: a stage is K, V and the second part of K'
+  static constexpr int kStage = (kState ? 3 : 2) * kTile;
+  static constexpr int kLo = kState ? 2 * kTile : kStages * kStage;   // kState: within the stage
+  static constexpr int kQ = kLo + kTile;
+  static constexpr int kS = kQ + kTile;
+  static constexpr int kSmem = 1024 + (kState ? kStages * kStage : kS + kTile);
   static constexpr int kCols = kState ? 128 : 512;
 };
 
@@ -228,7 +231,8 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
 struct Bars {
   uint64_t full[2], empty[2];
   uint64_t scores[2], p[2], out[2], drained[2], k[2], v[2], state[2];
-  uint64_t qk, upd, drain;
+  uint64_t q_full[2];
+  uint64_t q_read, qk, upd, drain;
 };
 
 struct Shared {
@@ -255,7 +259,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto tile_k = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage); };
   auto tile_v = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage + kTile); };
-  auto tile_q = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage + 2 * kTile); };
+  auto tile_lo = [&](int s) { return base + static_cast<uint32_t>((kState ? s * L::kStage : 0) + L::kLo); };
+  const uint32_t tile_q = base + static_cast<uint32_t>(L::kQ);
   const uint32_t tile_s = base + static_cast<uint32_t>(L::kS);
 
   const int sweep = blockIdx.z, h = blockIdx.y;
@@ -283,7 +288,9 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       mbar_init(smem_u32(&sh.bars.k[s]), kState ? 8 : 4);
       mbar_init(smem_u32(&sh.bars.v[s]), 4);
       mbar_init(smem_u32(&sh.bars.state[s]), 4);
+      mbar_init(smem_u32(&sh.bars.q_full[s]), 1);
     }
+    mbar_init(smem_u32(&sh.bars.q_read), 4);
     mbar_init(smem_u32(&sh.bars.qk), 1);
     mbar_init(smem_u32(&sh.bars.upd), 1);
     mbar_init(smem_u32(&sh.bars.drain), 1);
@@ -416,7 +423,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   };
   auto decay_k = [&](int chunk, int r, int panel, float f) {
     const uint32_t row = row_at(tile_k(chunk & 1) + panel * kPanel, r);
-    const uint32_t row2 = row_at(tile_q(chunk & 1) + panel * kPanel, r);
+    const uint32_t row2 = row_at(tile_lo(chunk & 1) + panel * kPanel, r);
     const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
     const __half fh = __float2half_rn(f);
     const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
@@ -451,25 +458,39 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       // ---------------------------------------------------------------------------- TMA
       const uint64_t pol = l2_policy_evict_normal();
       auto col = [&](int64_t stride) { return static_cast<int32_t>(h * stride); };
-      int issued = 0;
+      int issued = 0, q_issued = 0;
       for (int ch = 0; ch < chunks; ++ch) {
         const int s = ch & 1;
         if (ch >= 2 && !wait_bounded(smem_u32(&sh.bars.empty[s]), ((ch >> 1) - 1) & 1, abort_flag,
                                      c.status))
           break;
         const uint32_t bar = smem_u32(&sh.bars.full[s]);
-        mbar_arrive_expect_tx(bar, (kState ? 2 : 3) * kTile);
+        mbar_arrive_expect_tx(bar, 2 * kTile);
         const int32_t y = static_cast<int32_t>(row0(ch));
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          if (!kState) tma_load_2d(tile_q(s) + p * kPanel, mq, bar, col(w.q_h) + 64 * p, y, pol);
           tma_load_2d(tile_k(s) + p * kPanel, mk, bar, col(w.k_h) + 64 * p, y, pol);
           tma_load_2d(tile_v(s) + p * kPanel, mv, bar, col(w.v_h) + 64 * p, y, pol);
         }
         issued = ch + 1;
+        if constexpr (!kState) {
+          // Q has one place: the products and the row warps are done with the chunk before
+          if (ch > 0 && (!wait_bounded(smem_u32(&sh.bars.qk), (ch - 1) & 1, abort_flag, c.status) ||
+                         !wait_bounded(smem_u32(&sh.bars.q_read), (ch - 1) & 1, abort_flag, c.status)))
+            break;
+          const uint32_t qbar = smem_u32(&sh.bars.q_full[s]);
+          mbar_arrive_expect_tx(qbar, kTile);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            tma_load_2d(tile_q + p * kPanel, mq, qbar, col(w.q_h) + 64 * p, y, pol);
+          q_issued = ch + 1;
+        }
       }
       for (int ch = issued > 2 ? issued - 2 : 0; ch < issued; ++ch)   // all land before the block ends
         mbar_wait_bounded(smem_u32(&sh.bars.full[ch & 1]), (ch >> 1) & 1, kDrainNs, nullptr, c.status);
+      if (q_issued > 0)
+        mbar_wait_bounded(smem_u32(&sh.bars.q_full[(q_issued - 1) & 1]), ((q_issued - 1) >> 1) & 1,
+                          kDrainNs, nullptr, c.status);
     }
     if (warp == 1) {
     // ------------------------------------------------------------------------------ MMA
@@ -484,27 +505,28 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), 0);
-        product_mn(t_upd, tile_v(s), tile_q(s), 1);
+        product_mn(t_upd, tile_v(s), tile_lo(s), 1);
         commit(sh.bars.upd);
       } else {
         // scores, in P's place: the product that read it last has completed
-        ok = wait(sh.bars.full[s], ph) && (ch == 0 || wait(sh.bars.out[s ^ 1], ((ch - 1) >> 1) & 1));
+        ok = wait(sh.bars.full[s], ph) && wait(sh.bars.q_full[s], ph) &&
+             (ch == 0 || wait(sh.bars.out[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        product_kk(t_p, tile_q(s), tile_k(s));
+        product_kk(t_p, tile_q, tile_k(s));
         commit(sh.bars.scores[s]);
         // Q S: the state is in shared memory, and the outputs before are read
         ok = wait(sh.bars.state[s], ph) &&
              (ch == 0 || wait(sh.bars.drained[s ^ 1], ((ch - 1) >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        product_kk(t_qs, tile_q(s), tile_s);
+        product_kk(t_qs, tile_q, tile_s);
         commit(sh.bars.qk);
         ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph);
         if (!ok) break;
         tc_fence_after();
         product_mn(t_upd, tile_v(s), tile_k(s), 0);
-        product_mn(t_upd, tile_v(s), tile_q(s), 1);
+        product_mn(t_upd, tile_v(s), tile_lo(s), 1);
         commit(sh.bars.upd);
         ok = wait(sh.bars.p[s], ph);
         if (!ok) break;
@@ -633,7 +655,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         float f;
         if (!find_exp(ch, r, 0, 2, ok, &f)) break;
         arrive(sh.bars.v[s]);
-        if (!wait(sh.bars.qk, ch & 1)) break;   // K and Q are no longer read as such
+        // K is no longer read as such, nor the second part of the K' before
+        if (!wait(sh.bars.scores[s], ph) || (ch > 0 && !wait(sh.bars.upd, (ch - 1) & 1))) break;
         decay_k(ch, r, 0, f);
         arrive(sh.bars.k[s]);
       }
@@ -666,8 +689,9 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         const int ph = (ch >> 1) & 1;
         // The row's power of two, from a bound on its scores, 128 max|q_i| max|k|: a few bits more
         // than they have, of the 29 between fp16's largest and smallest normal values.
-        if (!wait(sh.bars.full[turn], ph)) break;
-        const float top_q = row_top(row_at(tile_q(turn), r));
+        if (!wait(sh.bars.q_full[turn], ph)) break;
+        const float top_q = row_top(row_at(tile_q, r));
+        arrive(sh.bars.q_read);
         if (!wait(sh.bars.v[turn], ph)) break;
         const int e = up_to_half(top_q * max8(sh.top_k[turn]) * (128.0f * fabsf(w.a)));
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
