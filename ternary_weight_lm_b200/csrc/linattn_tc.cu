@@ -269,7 +269,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
   const bool whole = g.first && g.last;
   if (!g.valid || (kState && whole)) return;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (broadcast, so that the roles' branches are known to be the same for a whole warp)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool back = w.backwards != 0;
   const int lag = back ? 1 : 0;
   const int chunks = static_cast<int>((g.n + kC - 1) / kC);
