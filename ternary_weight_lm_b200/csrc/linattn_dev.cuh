@@ -28,6 +28,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
   return v;
 }
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float v;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
+}
+
 // log2 of a head's decay.  Decays lie in [0, 1]: a logarithm above 0 (or not a number) counts
 // as 0, that of a decay of 0 is -inf.
 __device__ __forceinline__ double lin_lg2_of(float log_decay) {

@@ -173,26 +173,37 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   const uint32_t tile_p = base + static_cast<uint32_t>(kStages * kStage);
 
   const int64_t chunks = (g.n + kC - 1) / kC;
+  // A thread's vectors of a tile: one column of vectors, rows a multiple of eight apart (so that the
+  // swizzle is the same for all); pointers move on by a chunk at a time.
+  constexpr int kRowsK = kThreads / (DK / 8), kRowsV = kThreads / (DV / 8);
+  const int rk = tid / (DK / 8), rv = tid / (DV / 8);
+  const uint32_t at_k = tile_at<DK / 8>(0u, rk, tid % (DK / 8));
+  const uint32_t at_v = tile_at<DV / 8>(0u, rv, tid % (DV / 8));
+  const __half* next_k = kp + g.token(rk) * w.k_t + tid % (DK / 8) * 8;
+  const __half* next_q = qp + g.token(rk) * w.q_t + tid % (DK / 8) * 8;
+  const __half* next_v = vp + g.token(rv) * w.v_t + tid % (DV / 8) * 8;
+  const int64_t step_k = g.step * kRowsK * w.k_t, step_q = g.step * kRowsK * w.q_t;
+  const int64_t step_v = g.step * kRowsV * w.v_t;
   auto load = [&](int64_t chunk) {
     if (chunk < chunks) {
       const int s = static_cast<int>(chunk % kStages);
-      const int64_t p0 = chunk * kC;
+      const int left = static_cast<int>(min(static_cast<int64_t>(kC), g.n - chunk * kC));
 #pragma unroll
-      for (int i = 0; i < kC * DK / 8 / kThreads; ++i) {
-        const int x = tid + i * kThreads, r = x / (DK / 8), vec = x % (DK / 8);
-        const bool in = p0 + r < g.n;
-        const int64_t t = in ? g.token(p0 + r) : g.begin;
-        cp_async16(tile_at<DK / 8>(tile_k(s), r, vec), kp + t * w.k_t + vec * 8, in);
-        if constexpr (!kState)
-          cp_async16(tile_at<DK / 8>(tile_q(s), r, vec), qp + t * w.q_t + vec * 8, in);
+      for (int i = 0; i < kC / kRowsK; ++i) {
+        const bool in = rk + i * kRowsK < left;
+        const uint32_t at = at_k + static_cast<uint32_t>(i * kRowsK * DK * 2);
+        cp_async16(tile_k(s) + at, in ? next_k + i * step_k : kp, in);
+        if constexpr (!kState) cp_async16(tile_q(s) + at, in ? next_q + i * step_q : qp, in);
       }
 #pragma unroll
-      for (int i = 0; i < kC * DV / 8 / kThreads; ++i) {
-        const int x = tid + i * kThreads, r = x / (DV / 8), vec = x % (DV / 8);
-        const bool in = p0 + r < g.n;
-        const int64_t t = in ? g.token(p0 + r) : g.begin;
-        cp_async16(tile_at<DV / 8>(tile_v(s), r, vec), vp + t * w.v_t + vec * 8, in);
+      for (int i = 0; i < kC / kRowsV; ++i) {
+        const bool in = rv + i * kRowsV < left;
+        cp_async16(tile_v(s) + at_v + static_cast<uint32_t>(i * kRowsV * DV * 2),
+                   in ? next_v + i * step_v : vp, in);
       }
+      next_k += (kC / kRowsK) * step_k;
+      next_q += (kC / kRowsK) * step_q;
+      next_v += (kC / kRowsV) * step_v;
     }
     cp_async_commit();   // (possibly empty) one group for each chunk
   };
@@ -230,7 +241,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             }
           }
         }
-        uint32_t m[2] = {0u, 0u};
+        float m[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -238,14 +249,14 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             const int i = 16 * warp + gq + 8 * (e >> 1), d = i - (8 * j + 2 * t4 + (e & 1));
             // not a product with 0: the score of a later token may be anything
             P[j][e] = d >= 0 ? P[j][e] * (w.a * s_pow[d]) : 0.0f;
-            m[e >> 1] = max(m[e >> 1], magnitude(P[j][e]));
+            if (e & 1) m[e >> 1] = max3_abs(m[e >> 1], P[j][e - 1], P[j][e]);
           }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
-          m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
+          m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
+          m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
           const int row = 16 * warp + gq + 8 * r;
-          const int e = up_to_half(m[r], 40);
+          const int e = up_to_half(__float_as_uint(m[r]), 40);
           const float f = pow2(e);
           if (t4 == 0) s_exp[row] = e;
 #pragma unroll
@@ -347,6 +358,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
           }
         }
       }
+      __half* o_row = op + g.token(chunk * kC + gq) * w.o_t + 2 * t4;
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -354,7 +366,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
           const int i = 16 * m + gq + 8 * r;
           if (i < n) {
             const float f = w.b * pow2(-s_exp[i]);
-            __half* row = op + g.token(chunk * kC + i) * w.o_t + 2 * t4;
+            __half* row = o_row + (2 * m + r) * (8 * g.step * w.o_t);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
               *reinterpret_cast<uint32_t*>(row + 8 * v) =
@@ -418,7 +430,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
           }
       }
     const float decay = s_pow[n], back = pow2(-ev);
-    top = 0u;
+    float most = 0.0f;
     constexpr int NG = 4;             // column tiles of S^T at a time
 #pragma unroll
     for (int n0 = 0; n0 < NK; n0 += NG) {
@@ -454,9 +466,12 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
           for (int e = 0; e < 4; ++e) {
             float& y = S[m][n0 + x][e];
             y = fmaf(decay, y, D[m][x][e] * back);
-            if constexpr (!kState) top = max(top, magnitude(y));
+            if constexpr (!kState) {
+              if (e & 1) most = max3_abs(most, S[m][n0 + x][e - 1], y);
+            }
           }
     }
+    if constexpr (!kState) top = __float_as_uint(most);
   }
   cp_async_wait<0>();
 

@@ -139,13 +139,6 @@ __device__ __forceinline__ void product_tm(uint32_t d, uint32_t a, uint32_t b) {
       : "memory");
 }
 
-// max(|a|, |b|, |c|)
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float v;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
-  return v;
-}
-
 __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
