@@ -323,8 +323,9 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  * Shapes: 1 <= T <= 16777216, 1 <= B <= 2^20, 1 <= H <= 4096, dk and dv multiples of 8 from 8 to
  * 256.  Pointers to matrices are 16-byte aligned, ws is 256-byte aligned (NULL with ws_bytes 0
  * when the query gives 0).  The workspace holds nothing between calls; calls that may overlap
- * need one each.  Errors as for the forward.  Asynchronous on `stream`; may be captured into a
- * CUDA graph. */
+ * need one each.  Outputs overlap no input (but hT may be h0).  A value that is not finite reaches
+ * no earlier token and no other sequence; what depends on it is not finite.  Errors as for the
+ * forward.  Asynchronous on `stream`; may be captured into a CUDA graph. */
 typedef struct {
   int64_t T;                    /* tokens of all sequences */
   int64_t B;                    /* sequences */
@@ -351,8 +352,8 @@ mmf_status mmf_linattn_forward(const mmf_linattn_desc* d, const void* q, const v
  *   R_t = U + scale q_t dout_t^T,  U = gamma R_t, last token first, U = dhT at the start
  *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dh0 = U at the end
  * h0: as for the forward.  dq, dk [T x H x dk] and dv [T x H x dv] are contiguous, one row for
- * each head (of a row shared by heads the caller adds them up); dh0 (or NULL) fp32, not dhT
- * itself.  log_decay is a constant: it gets no gradient. */
+ * each head (of a row shared by heads the caller adds them up); dh0 (or NULL) fp32, neither dhT
+ * nor h0 itself.  log_decay is a constant: it gets no gradient. */
 mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void* q, const void* k,
                                 const void* v, const void* dout, const float* h0,
                                 const float* dhT, void* dq, void* dk, void* dv, float* dh0,

@@ -134,7 +134,11 @@ __device__ __forceinline__ LinSeg lin_find(const LinCall& c, int64_t x, bool bac
   LinSeg g = {};
   int64_t lo = 0, hi = 0, k = 0;
   bool bad = false;
-  if (c.cu == nullptr) {
+  if (!c.split) {   // one item for each sequence
+    g.seq = static_cast<int>(x);
+    lin_bounds(c, g.seq, &lo, &hi, &bad);
+    if (bad) atomicOr(c.status, kStatusBadPlan);
+  } else if (c.cu == nullptr) {
     const int64_t per = lin_count(c, c.T / c.B);
     g.seq = static_cast<int>(x / per);
     k = x - g.seq * per;

@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "linattn.cuh"
 #include "linattn_dev.cuh"
@@ -218,6 +219,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
     cp_async_wait<kStages - 2>();
     __syncthreads();                  // the chunk is in, and the one before it is done with
     load(chunk + kStages - 1);
+    bool strange = false;             // the warp's part of V has a value that is not finite
 
     if constexpr (!kState) {
       // ---- scores: warp = 16 rows, the column tiles up to its diagonal
@@ -325,6 +327,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             sum = __hfma2(*reinterpret_cast<const __half2*>(&b[v][z]), __float2half2_rn(0.0f), sum);
         }
         const bool odd = __any_sync(0xffffffffu, !__hbeq2(sum, __float2half2_rn(0.0f)));
+        strange |= odd;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           if (m < kk) continue;
@@ -390,22 +393,45 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
     // product to 2^14 .. 2^15, or the largest factor of a token that is not zero if that is less.
     auto weight = [&](int j) { return w.a * s_pow[max(n - 1 - j + lag, 0)]; };   // v is 0 past n
     float vtop = 0.0f, wide = 0.0f;
+    auto scan = [&](auto clean) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+      for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        __half2 m2 = __float2half2_rn(0.0f);
+        for (int z = 0; z < 2; ++z) {
+          __half2 m2 = __float2half2_rn(0.0f);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t u = hi[kk][m][2 * z + y];
+              if constexpr (clean.value)
+                u &= ((u & 0x7c00u) == 0x7c00u ? 0u : 0xffffu) |
+                     ((u & 0x7c000000u) == 0x7c000000u ? 0u : 0xffff0000u);
+              m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __half2*>(&u)));
+            }
+          const float2 x = __half22float2(m2);
+          const int j = 16 * kk + 2 * t4 + 8 * z;
+          const float w0 = fabsf(weight(j)), w1 = fabsf(weight(j + 1));
+          vtop = fmaxf(vtop, fmaxf(x.x * w0, x.y * w1));
+          wide = fmaxf(wide, fmaxf(x.x != 0.0f ? w0 : 0.0f, x.y != 0.0f ? w1 : 0.0f));
+        }
+    };
+    if constexpr (kState) {
+      __half2 check = __float2half2_rn(0.0f);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-            m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __half2*>(&hi[kk][m][2 * z + y])));
-        const float2 x = __half22float2(m2);
-        const int j = 16 * kk + 2 * t4 + 8 * z;
-        const float w0 = fabsf(weight(j)), w1 = fabsf(weight(j + 1));
-        vtop = fmaxf(vtop, fmaxf(x.x * w0, x.y * w1));
-        wide = fmaxf(wide, fmaxf(x.x != 0.0f ? w0 : 0.0f, x.y != 0.0f ? w1 : 0.0f));
-      }
+          for (int z = 0; z < 4; ++z)
+            check = __hfma2(*reinterpret_cast<const __half2*>(&hi[kk][m][z]), __float2half2_rn(0.0f), check);
+      strange = __any_sync(0xffffffffu, !__hbeq2(check, __float2half2_rn(0.0f)));
+    }
+    // the scale comes from what is finite: the rest stays as it is under any
+    if (strange)
+      scan(std::true_type{});
+    else
+      scan(std::false_type{});
     const int ev = min(up_to_half(__reduce_max_sync(0xffffffffu, magnitude(vtop)), 60),
                        up_to_half(__reduce_max_sync(0xffffffffu, magnitude(wide)), 60));
     const float fv = pow2(ev);

@@ -399,7 +399,18 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float wt = in ? w.a * sh.pow[n - 1 - pos + lag] : 0.0f;
     float top = 0.0f;
     if (ok && in) top = row_top(row_at(tile_k(chunk & 1) + panel * kPanel, r));
-    if (!(top <= 65504.0f)) sh.any_bad = 1;
+    if (!(top <= 65504.0f)) {
+      // the scales come from what is finite: the rest stays as it is under any of them
+      sh.any_bad = 1;
+      top = 0.0f;
+      const uint32_t row = row_at(tile_k(chunk & 1) + panel * kPanel, r);
+#pragma unroll 1
+      for (int x = 0; x < 8 * kVecs; ++x) {
+        uint16_t y;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(y) : "r"(vec_of(row, x >> 3) + 2u * (x & 7)) : "memory");
+        if ((y & 0x7c00u) != 0x7c00u) top = fmaxf(top, fabsf(__half2float(__ushort_as_half(y))));
+      }
+    }
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
     const float most = warp_max(top);
     top = warp_max(top * fabsf(wt));

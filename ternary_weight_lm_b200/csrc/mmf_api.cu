@@ -577,7 +577,9 @@ mmf_status check_out_strides(int64_t t, int64_t h, int64_t nt, int64_t nh, int64
   return MMF_OK;
 }
 
-mmf_status check_desc(const mmf_linattn_desc* d) {
+// Checks a descriptor and copies it to *n, with the stride of a dimension of one, which says
+// nothing, as a contiguous tensor has it.
+mmf_status check_desc(const mmf_linattn_desc* d, mmf_linattn_desc* n) {
   if (!d || !d->log_decay || check_dtype(d->dt) != MMF_OK) return MMF_ERR_INVALID_ARG;
   if (!(d->scale == d->scale) || d->scale - d->scale != 0.0f) return MMF_ERR_INVALID_ARG;
   mmf_status st;
@@ -586,10 +588,19 @@ mmf_status check_desc(const mmf_linattn_desc* d) {
   if (!d->cu_seqlens && d->T % d->B != 0) return MMF_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(d->log_decay, 4) || (d->cu_seqlens && !aligned(d->cu_seqlens, 4)))
     return MMF_ERR_ALIGNMENT;
-  if ((st = check_strides(d->q_t, d->q_h, d->dt)) != MMF_OK ||
-      (st = check_strides(d->k_t, d->k_h, d->dt)) != MMF_OK ||
-      (st = check_strides(d->v_t, d->v_h, d->dt)) != MMF_OK ||
-      (st = check_out_strides(d->o_t, d->o_h, d->T, d->H, d->dv, d->dt)) != MMF_OK)
+  *n = *d;
+  if (d->H == 1) {
+    n->q_h = n->k_h = d->dk;
+    n->v_h = n->o_h = d->dv;
+  }
+  if (d->T == 1) {
+    n->q_t = n->k_t = static_cast<int64_t>(d->H) * d->dk;
+    n->v_t = n->o_t = static_cast<int64_t>(d->H) * d->dv;
+  }
+  if ((st = check_strides(n->q_t, n->q_h, d->dt)) != MMF_OK ||
+      (st = check_strides(n->k_t, n->k_h, d->dt)) != MMF_OK ||
+      (st = check_strides(n->v_t, n->v_h, d->dt)) != MMF_OK ||
+      (st = check_out_strides(n->o_t, n->o_h, d->T, d->H, d->dv, d->dt)) != MMF_OK)
     return st;
   return MMF_OK;
 }
@@ -636,11 +647,13 @@ MMF_EXPORT size_t mmf_linattn_backward_workspace_bytes(const mmf_linattn_desc* d
   return lin_ws_bytes(d, 3);
 }
 
-MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* d, const void* q, const void* k,
+MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* desc, const void* q, const void* k,
                                           const void* v, const float* h0, void* o, float* hT,
                                           void* ws, size_t ws_bytes, void* stream) {
   if (!q || !k || !v || !o) return MMF_ERR_INVALID_ARG;
-  mmf_status st = check_desc(d);
+  mmf_linattn_desc checked;
+  const mmf_linattn_desc* d = &checked;
+  mmf_status st = check_desc(desc, &checked);
   if (st != MMF_OK) return st;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
       (h0 && !aligned(h0, 16)) || (hT && !aligned(hT, 16)))
@@ -673,13 +686,15 @@ MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* d, const void*
   return from_cuda(launch_linattn(c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-MMF_EXPORT mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void* q, const void* k,
+MMF_EXPORT mmf_status mmf_linattn_backward(const mmf_linattn_desc* desc, const void* q, const void* k,
                                            const void* v, const void* dout, const float* h0,
                                            const float* dhT, void* dq, void* dk, void* dv,
                                            float* dh0, void* ws, size_t ws_bytes, void* stream) {
   if (!q || !k || !v || !dout || !dq || !dk || !dv) return MMF_ERR_INVALID_ARG;
-  if (dh0 && dh0 == dhT) return MMF_ERR_INVALID_ARG;
-  mmf_status st = check_desc(d);
+  if (dh0 && (dh0 == dhT || dh0 == h0)) return MMF_ERR_INVALID_ARG;
+  mmf_linattn_desc checked;
+  const mmf_linattn_desc* d = &checked;
+  mmf_status st = check_desc(desc, &checked);
   if (st != MMF_OK) return st;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dout, 16) ||
       !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || (h0 && !aligned(h0, 16)) ||
@@ -759,11 +774,13 @@ MMF_EXPORT mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void
   return from_cuda(launch_linattn(c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-MMF_EXPORT mmf_status mmf_linattn_step(const mmf_linattn_desc* d, const void* q, const void* k,
+MMF_EXPORT mmf_status mmf_linattn_step(const mmf_linattn_desc* desc, const void* q, const void* k,
                                        const void* v, void* o, float* state, const int32_t* slots,
                                        int64_t n_slots, void* stream) {
   if (!q || !k || !v || !o || !state) return MMF_ERR_INVALID_ARG;
-  mmf_status st = check_desc(d);
+  mmf_linattn_desc checked;
+  const mmf_linattn_desc* d = &checked;
+  mmf_status st = check_desc(desc, &checked);
   if (st != MMF_OK) return st;
   if (d->cu_seqlens || d->T != d->B) return MMF_ERR_INVALID_ARG;
   if (slots ? (n_slots < 1 || n_slots > kMaxBatch) : n_slots != 0) return MMF_ERR_INVALID_ARG;

@@ -67,10 +67,14 @@ def linattn_backward(q, k, v, log_decay, cu, scale, do, h0=None, dhT=None):
 
 
 def absolute(f, *args, **kw):
-    """The same with every value's magnitude: a bound on the sum of the magnitudes of a result's
-    terms, which its rounding errors are relative to."""
-    return f(*(np.abs(a) if isinstance(a, np.ndarray) and a.dtype.kind == "f" and i != 3 else a
-               for i, a in enumerate(args)),
+    """The same with every value's magnitude (the scale's too, the logarithms of decays as they
+    are): a bound on the sum of the magnitudes of a result's terms, which its rounding errors are
+    relative to."""
+    def mag(i, a):
+        if isinstance(a, float):
+            return abs(a)
+        return np.abs(a) if isinstance(a, np.ndarray) and a.dtype.kind == "f" and i != 3 else a
+    return f(*(mag(i, a) for i, a in enumerate(args)),
              **{n: None if a is None else np.abs(a) for n, a in kw.items()})
 
 

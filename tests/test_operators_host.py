@@ -126,6 +126,8 @@ def test_linattn_workspaces_and_aliases_are_refused():
     assert L.mmf_linattn_backward(*args, A16 + 256, A16, need - 1, None) == WS
     # the gradients of the first and of the last state are read and written at unlike times
     assert L.mmf_linattn_backward(*args, A16, A16, need, None) == INVALID
+    args = (r, A16, A16, A16, A16, A16, None, A16, A16, A16)
+    assert L.mmf_linattn_backward(*args, A16, A16, need, None) == INVALID
     # one short sequence needs none, and a size without a workspace is refused
     d = desc(T=100, B=1)
     assert mmf.mmf_linattn_workspace_bytes(d) == 0
