@@ -8,7 +8,10 @@
 // The contraction keeps the orientation of the ternary one: the MMA's M side is 128 weight rows,
 // its N side BN tokens, so that a single token costs one narrow MMA.  The codes are int8 already,
 // so both operands go from TMA to shared memory to tcgen05.mma (kind::i8) untouched, and the
-// only other work is the epilogue.  Few tokens: bound by the weight stream (N K bytes once).
+// only other work is the epilogue.  Few tokens: bound by the weight stream (N K bytes once).  Measured
+// back to back: one token, 2048 -> 32000, 9.0 us (65.5 MB, part of it from L2); 64 tokens, 2048 ->
+// 11264, 9.9 us; many tokens on the CTA pairs, 8192 x 2048 -> 11264, 127 us, 91 % of twice the bf16
+// rate.
 #include <cuda_fp16.h>
 
 #include <mutex>
@@ -23,6 +26,8 @@ namespace {
 // A block takes kHeld / V rows at a time, a thread V vectors of eight values of each, held in
 // registers between the maximum and the encoding: 32 to 64 KB in flight whatever the row's length.
 // Rows of more than 4096 values are taken one at a time, beyond kHeld vectors read again (from L2).
+// Bound by the stream: 32000 x 2048 in fp32 take 58 us, 86 % of a copy's rate (72 us with one row a
+// block and a division for every value).
 constexpr int kQThreads = 128;
 constexpr int kHeld = 8;
 
