@@ -481,97 +481,91 @@ def _tensor(name, t, shape, dtypes, device, contiguous=True):
     if got != shape and (len(got) != len(shape) or
                          any(s is not None and s != n for s, n in zip(shape, got))):
         raise ValueError(f"{name}: shape {tuple(got)}, expected {shape}")
+    if t.is_contiguous():
+        return
     if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif got[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    if got[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
-class _On:
-    """Makes a tensor's device and the call's stream current, so that what the call allocates
-    belongs to the stream that uses it; ``handle`` is the stream's."""
-    __slots__ = ("device", "given", "stream", "handle")
-
-    def __init__(self, t, stream):
-        import torch
-        if not t.is_cuda:
-            raise ValueError(f"tensors must be on a GPU, got {t.device}")
-        at = t.get_device()
-        self.device = self.stream = None
-        if at != torch._C._cuda_getDevice():
-            self.device = torch.cuda.device(at)
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(at)
-        elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        self.given = stream
-
-    def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.given is not None:
-            import torch
-            self.stream = torch.cuda.stream(self.given)
-            self.stream.__enter__()
-            self.handle = self.given.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+def _on(t, stream, call):
+    """``call(handle)`` with the tensor's device and the call's stream current, so that what the
+    call allocates belongs to the stream that uses it; the handle is the stream's."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a GPU, got {t.device}")
+    at = t.get_device()
+    if stream is None:
+        if at == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(at))
+        with torch.cuda.device(at):
+            return call(torch._C._cuda_getCurrentRawStream(at))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    with torch.cuda.device(at), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def quantize_weights_int8(W, stream=None):
     """W [N, K] (fp32/fp16, CUDA, contiguous) -> (W8 int8 [N, K], wscale float32 [N])."""
     import torch
-    _tensor("W", W, (None, None), (torch.float32, torch.float16), W.device)
-    with _On(W, stream) as on:
-        W8 = torch.empty(W.shape, dtype=torch.int8, device=W.device)
-        wscale = torch.empty(W.shape[0], dtype=torch.float32, device=W.device)
-        mmf_int8_quantize_weights(W, W8, wscale, on.handle)
-    return W8, wscale
+    dev = W.device
+    _tensor("W", W, (None, None), (torch.float32, torch.float16), dev)
+
+    def call(handle):
+        W8 = torch.empty(W.shape, dtype=torch.int8, device=dev)
+        wscale = torch.empty(W.shape[0], dtype=torch.float32, device=dev)
+        mmf_int8_quantize_weights(W, W8, wscale, handle)
+        return W8, wscale
+
+    return _on(W, stream, call)
 
 
 def int8_matmul(A, gamma, W8, wscale, out_dtype=None, out=None, stream=None):
     """y [T, N] of activation codes A [T, K] with scales gamma [T] (mmf_quantize_activations) and
     weights from quantize_weights_int8; fp16 unless out_dtype or out says otherwise."""
     import torch
-    _tensor("A", A, (None, None), (torch.int8,), A.device)
+    dev = A.device
+    _tensor("A", A, (None, None), (torch.int8,), dev)
     T, K = A.shape
-    _tensor("W8", W8, (None, K), (torch.int8,), A.device)
+    _tensor("W8", W8, (None, K), (torch.int8,), dev)
     N = W8.shape[0]
-    _tensor("gamma", gamma, (T,), (torch.float32,), A.device)
-    _tensor("wscale", wscale, (N,), (torch.float32,), A.device)
+    _tensor("gamma", gamma, (T,), (torch.float32,), dev)
+    _tensor("wscale", wscale, (N,), (torch.float32,), dev)
     if out is not None:
-        _tensor("out", out, (T, N), (torch.float32, torch.float16), A.device)
-    with _On(A, stream) as on:
-        if out is None:
-            out = torch.empty((T, N), dtype=out_dtype or torch.float16, device=A.device)
-        mmf_int8_forward_quantized(A, gamma, W8, wscale, out, on.handle)
-    return out
+        _tensor("out", out, (T, N), (torch.float32, torch.float16), dev)
+
+    def call(handle):
+        y = out
+        if y is None:
+            y = torch.empty((T, N), dtype=out_dtype or torch.float16, device=dev)
+        mmf_int8_forward_quantized(A, gamma, W8, wscale, y, handle)
+        return y
+
+    return _on(A, stream, call)
 
 
 def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws=None,
                         stream=None):
     """RMSNorm, activation quantisation and 8-bit product of x [T, K]: y [T, N]."""
     import torch
-    f = (torch.float32, torch.float16)
-    _tensor("x", x, (None, None), f, x.device)
+    dev = x.device
+    _tensor("x", x, (None, None), (torch.float32, torch.float16), dev)
     T, K = x.shape
-    _tensor("W8", W8, (None, K), (torch.int8,), x.device)
+    _tensor("W8", W8, (None, K), (torch.int8,), dev)
     N = W8.shape[0]
-    _tensor("wscale", wscale, (N,), (torch.float32,), x.device)
+    _tensor("wscale", wscale, (N,), (torch.float32,), dev)
     if norm_w is not None:
-        _tensor("norm_w", norm_w, (K,), (torch.float32,), x.device)
-    with _On(x, stream) as on:
-        y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
-        if ws is None:
-            ws = workspace(mmf_int8_workspace_bytes(T, K), x.device)
-        mmf_int8_forward(x, norm_w, eps, W8, wscale, y, ws, on.handle)
-    return y
+        _tensor("norm_w", norm_w, (K,), (torch.float32,), dev)
+
+    def call(handle):
+        y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
+        scratch = workspace(mmf_int8_workspace_bytes(T, K), dev) if ws is None else ws
+        mmf_int8_forward(x, norm_w, eps, W8, wscale, y, scratch, handle)
+        return y
+
+    return _on(x, stream, call)
 
 
 def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
@@ -601,6 +595,13 @@ def _linattn_ws(ws, need, device):
     return ws if ws is not None or need == 0 else workspace(need, device)
 
 
+def _linattn_states(d, device, **states):
+    import torch
+    for name, t in states.items():
+        if t is not None:
+            _tensor(name, t, (d.B, d.H, d.dk, d.dv), (torch.float32,), device)
+
+
 def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None, h0=None, hT=None,
                     out=None, ws=None, stream=None):
     """Linear attention with a decay for each head over packed prompts: o [T, H, dv].
@@ -611,17 +612,19 @@ def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None,
     [B, H, dk, dv] fp32: states before (zero unless given) and after (written if given; may be
     h0)."""
     import torch
+    dev = q.device
     d = _linattn(q, k, v, log_decay, out, scale, cu_seqlens, batch)
-    state = (d.B, d.H, d.dk, d.dv)
-    for name, t in (("h0", h0), ("hT", hT)):
-        if t is not None:
-            _tensor(name, t, state, (torch.float32,), q.device)
-    with _On(q, stream) as on:
-        if out is None:
-            out = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
-        ws = _linattn_ws(ws, mmf_linattn_workspace_bytes(d), q.device)
-        mmf_linattn_forward(d, q, k, v, h0, out, hT, ws, on.handle)
-    return out
+    _linattn_states(d, dev, h0=h0, hT=hT)
+
+    def call(handle):
+        o = out
+        if o is None:
+            o = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=dev)
+        scratch = _linattn_ws(ws, mmf_linattn_workspace_bytes(d), dev)
+        mmf_linattn_forward(d, q, k, v, h0, o, hT, scratch, handle)
+        return o
+
+    return _on(q, stream, call)
 
 
 def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, stream=None):
@@ -630,16 +633,21 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, st
     state [B, H, dk, dv] fp32 is updated in place; with slots [B] int32 (device) it is a pool
     [n, H, dk, dv] and slots names each row's state (negative: padding, zeros out)."""
     import torch
+    dev = q.device
     d = _linattn(q, k, v, log_decay, out, scale, None, q.shape[0])
-    _tensor("state", state, (None if slots is not None else d.B, d.H, d.dk, d.dv), (torch.float32,),
-            q.device)
+    _tensor("state", state, (None if slots is not None else d.B, d.H, d.dk, d.dv),
+            (torch.float32,), dev)
     if slots is not None:
-        _tensor("slots", slots, (d.B,), (torch.int32,), q.device)
-    with _On(q, stream) as on:
-        if out is None:
-            out = torch.empty((d.B, d.H, d.dv), dtype=q.dtype, device=q.device)
-        mmf_linattn_step(d, q, k, v, out, state, slots, on.handle)
-    return out
+        _tensor("slots", slots, (d.B,), (torch.int32,), dev)
+
+    def call(handle):
+        o = out
+        if o is None:
+            o = torch.empty((d.B, d.H, d.dv), dtype=q.dtype, device=dev)
+        mmf_linattn_step(d, q, k, v, o, state, slots, handle)
+        return o
+
+    return _on(q, stream, call)
 
 
 def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batch=None, h0=None,
@@ -649,15 +657,18 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batc
     dout [T, H, dv]: the gradient of o; dhT: that of hT (none unless given).  Rows of tokens
     outside the sequences are not written."""
     import torch
+    dev = q.device
     d = _linattn(q, k, v, log_decay, dout, scale, cu_seqlens, batch)
-    state = (d.B, d.H, d.dk, d.dv)
-    for name, t in (("h0", h0), ("dhT", dhT)):
-        if t is not None:
-            _tensor(name, t, state, (torch.float32,), q.device)
-    with _On(q, stream) as on:
-        dq, dk = (torch.empty((d.T, d.H, d.dk), dtype=q.dtype, device=q.device) for _ in range(2))
-        dv = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
-        dh0 = torch.empty(state, dtype=torch.float32, device=q.device) if want_dh0 else None
-        ws = _linattn_ws(ws, mmf_linattn_backward_workspace_bytes(d), q.device)
-        mmf_linattn_backward(d, q, k, v, dout, h0, dhT, dq, dk, dv, dh0, ws, on.handle)
-    return dq, dk, dv, dh0
+    _linattn_states(d, dev, h0=h0, dhT=dhT)
+
+    def call(handle):
+        dq, dk = (torch.empty((d.T, d.H, d.dk), dtype=q.dtype, device=dev) for _ in range(2))
+        dv = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=dev)
+        dh0 = None
+        if want_dh0:
+            dh0 = torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=dev)
+        scratch = _linattn_ws(ws, mmf_linattn_backward_workspace_bytes(d), dev)
+        mmf_linattn_backward(d, q, k, v, dout, h0, dhT, dq, dk, dv, dh0, scratch, handle)
+        return dq, dk, dv, dh0
+
+    return _on(q, stream, call)
