@@ -49,6 +49,12 @@ __device__ __forceinline__ float lin_power(double lg2, int64_t n) {
   return n == 0 ? 1.0f : exp2f(static_cast<float>(lg2 * static_cast<double>(n)));
 }
 
+// An infinity in a start state as a NaN, which the maxima that scales come from pass over: neither
+// leaves its column finite, but an infinity would take the range from the other columns.
+__device__ __forceinline__ float lin_nan_if_inf(float x) {
+  return isinf(x) ? __int_as_float(0x7fffffff) : x;
+}
+
 // A head's decay token by token.  gamma rounded to float is off by up to 2^-25, the same way every
 // time, which 512 tokens would raise to 10^-5 of a state.  So the two floats around gamma take
 // turns, in proportion: their products stay within one rounding of gamma's powers.

@@ -157,17 +157,18 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = v0 + 16 * m + gq + 8 * (e >> 1), col = 8 * n + 2 * t4 + (e & 1);
-          S[m][n][e] = from ? from[col * sk + row * sv] : 0.0f;
+          const float x = from ? from[col * sk + row * sv] : 0.0f;
+          S[m][n][e] = g.n > 0 ? lin_nan_if_inf(x) : x;
         }
   }
-  uint32_t top = 0u;                  // largest magnitude of the warp's state, as bits
+  float top = 0.0f;                   // largest magnitude of the state (but for NaN)
   if constexpr (!kState) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, magnitude(S[m][n][e]));
+        for (int e = 0; e < 4; e += 2) top = max3_abs(top, S[m][n][e], S[m][n][e + 1]);
   }
 
   const __half* kp = static_cast<const __half*>(w.k) + h * w.k_h;
@@ -285,8 +286,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int e = 0; e < 4; ++e) O[m][v][e] = 0.0f;
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int es = up_to_half(top, 60);
+      const int es = up_to_half(__reduce_max_sync(0xffffffffu, __float_as_uint(top)), 60);
       const float fs = pow2(es);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
@@ -463,7 +463,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
           }
       }
     const float decay = s_pow[n], back = pow2(-ev);
-    float most = 0.0f;
+    top = 0.0f;
     constexpr int NG = 4;             // column tiles of S^T at a time
 #pragma unroll
     for (int n0 = 0; n0 < NK; n0 += NG) {
@@ -500,11 +500,10 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             float& y = S[m][n0 + x][e];
             y = fmaf(decay, y, D[m][x][e] * back);
             if constexpr (!kState) {
-              if (e & 1) most = max3_abs(most, S[m][n0 + x][e - 1], y);
+              if (e & 1) top = max3_abs(top, S[m][n0 + x][e - 1], y);
             }
           }
     }
-    if constexpr (!kState) top = __float_as_uint(most);
   }
   cp_async_wait<0>();
 

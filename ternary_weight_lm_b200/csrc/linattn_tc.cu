@@ -376,11 +376,6 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     }
     fence_proxy_async_smem();
   };
-  // Row r of K' from row r of K: a gamma^(tokens after it) k_j in two fp16 parts, scaled by the
-  // chunk's power of two.  With the factor w 2^e = wh + wl in fp16, hi = k wh rounded, and the rest
-  // (k wh - hi, exact, plus k wl) is lo: three half2 operations, an error of about 2^-22.  e brings
-  // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
-  // that is less.
   // Largest magnitude in row r of a tile of K or Q, infinity or NaN if one of it is not finite.
   constexpr int kVecs = kState ? 8 : 16;   // vectors of a row that a thread takes (kState: a panel)
   auto row_top = [&](uint32_t row) {
@@ -397,7 +392,12 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float2 y = __half22float2(__hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3])));
     return y.x >= y.y || y.x != y.x ? y.x : y.y;
   };
-  // find_exp: e and row r's factor; false if one of the warps gave up (`ok`).  Named barrier `id` is
+  // Row r of K' from row r of K: a gamma^(tokens after it) k_j in two fp16 parts, scaled by the
+  // chunk's power of two.  With the factor w 2^e = wh + wl in fp16, hi = k wh rounded, and the rest
+  // (k wh - hi, exact, plus k wl) is lo: three half2 operations, an error of about 2^-22.  e brings
+  // the largest product to 2^14 .. 2^15, or the largest factor of a row that is not zero there if
+  // that is less.
+  // find_exp: e and row r's factor w 2^e; false if one of the warps gave up (`ok`).  Named barrier `id` is
   // that of the threads that share the tile: a group, or two with a panel each.
   auto find_exp = [&](int chunk, int r, int panel, int id, bool ok, float* f) {
     const int set = chunk & 1;   // written again only after all of them handed the chunk over
@@ -505,52 +505,52 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
                           kDrainNs, nullptr, c.status);
     }
     if (warp == 1) {
-    // ------------------------------------------------------------------------------ MMA
-    auto commit = [&](uint64_t& bar) { tc_commit_warp(smem_u32(&bar)); };
-    bool ok = true;
-    for (int ch = 0; ok && ch < chunks; ++ch) {
-      const int s = ch & 1, ph = (ch >> 1) & 1;
-      if constexpr (kState) {
-        // K' and V are ready, and the update before is read
-        ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph) &&
-             (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        product_mn(t_upd, tile_v(s), tile_k(s), 0);
-        product_mn(t_upd, tile_v(s), tile_lo(s), 1);
-        commit(sh.bars.upd);
-      } else {
-        // scores, in P's place: the product that read it last has completed
-        ok = wait(sh.bars.full[s], ph) && wait(sh.bars.q_full[s], ph) &&
-             (ch == 0 || wait(sh.bars.out[s ^ 1], ((ch - 1) >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        product_kk(t_p, tile_q, tile_k(s));
-        commit(sh.bars.scores[s]);
-        // Q S: the state is in shared memory, and the outputs before are read
-        ok = wait(sh.bars.state[s], ph) &&
-             (ch == 0 || wait(sh.bars.drained[s ^ 1], ((ch - 1) >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        product_kk(t_qs, tile_q, tile_s);
-        commit(sh.bars.qk);
-        ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph);
-        if (!ok) break;
-        tc_fence_after();
-        product_mn(t_upd, tile_v(s), tile_k(s), 0);
-        product_mn(t_upd, tile_v(s), tile_lo(s), 1);
-        commit(sh.bars.upd);
-        ok = wait(sh.bars.p[s], ph);
-        if (!ok) break;
-        tc_fence_after();
-        product_tm(t_pv, t_p, tile_v(s));
-        commit(sh.bars.out[s]);
-      }
-      commit(sh.bars.empty[s]);
+      // ---------------------------------------------------------------------------- MMA
+      auto commit = [&](uint64_t& bar) { tc_commit_warp(smem_u32(&bar)); };
+      bool ok = true;
+      for (int ch = 0; ok && ch < chunks; ++ch) {
+        const int s = ch & 1, ph = (ch >> 1) & 1;
+        if constexpr (kState) {
+          // K' and V are ready, and the update before is read
+          ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph) &&
+               (ch == 0 || wait(sh.bars.state[s ^ 1], ((ch - 1) >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          product_mn(t_upd, tile_v(s), tile_k(s), 0);
+          product_mn(t_upd, tile_v(s), tile_lo(s), 1);
+          commit(sh.bars.upd);
+        } else {
+          // scores, in P's place: the product that read it last has completed
+          ok = wait(sh.bars.full[s], ph) && wait(sh.bars.q_full[s], ph) &&
+               (ch == 0 || wait(sh.bars.out[s ^ 1], ((ch - 1) >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          product_kk(t_p, tile_q, tile_k(s));
+          commit(sh.bars.scores[s]);
+          // Q S: the state is in shared memory, and the outputs before are read
+          ok = wait(sh.bars.state[s], ph) &&
+               (ch == 0 || wait(sh.bars.drained[s ^ 1], ((ch - 1) >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          product_kk(t_qs, tile_q, tile_s);
+          commit(sh.bars.qk);
+          ok = wait(sh.bars.v[s], ph) && wait(sh.bars.k[s], ph);
+          if (!ok) break;
+          tc_fence_after();
+          product_mn(t_upd, tile_v(s), tile_k(s), 0);
+          product_mn(t_upd, tile_v(s), tile_lo(s), 1);
+          commit(sh.bars.upd);
+          ok = wait(sh.bars.p[s], ph);
+          if (!ok) break;
+          tc_fence_after();
+          product_tm(t_pv, t_p, tile_v(s));
+          commit(sh.bars.out[s]);
+        }
+        commit(sh.bars.empty[s]);
     }
-    commit(sh.bars.drain);
-    mbar_wait_bounded(smem_u32(&sh.bars.drain), 0, kDrainNs, nullptr, c.status);
-    __syncwarp();
+      commit(sh.bars.drain);
+      mbar_wait_bounded(smem_u32(&sh.bars.drain), 0, kDrainNs, nullptr, c.status);
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------------------ state
@@ -571,8 +571,11 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         sv = static_cast<size_t>(w.s_val);
       }
 #pragma unroll
-      for (int i = 0; i < kD / 2; ++i)
-        S[i] = from ? pair(from[2 * i * sk + r * sv], from[(2 * i + 1) * sk + r * sv]) : 0ull;
+      for (int i = 0; i < kD / 2; ++i) {
+        const float x = from ? from[2 * i * sk + r * sv] : 0.0f;
+        const float y = from ? from[(2 * i + 1) * sk + r * sv] : 0.0f;
+        S[i] = chunks > 0 ? pair(lin_nan_if_inf(x), lin_nan_if_inf(y)) : pair(x, y);
+      }
     }
     float top[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (!kState) {

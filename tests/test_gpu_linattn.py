@@ -120,17 +120,25 @@ def test_infinities_and_nan_stay_in_their_sequence(d):
     assert not np.isfinite(o[90:270]).any()
 
 
+# in one segment, and in the first of several; or in the state that the prompt starts from
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
 @pytest.mark.parametrize("d", [64, 128, 40])
-def test_a_bad_value_stays_in_its_column(d, bad):
-    T, H, lg, at, col = 300, 2, _decays(2), 141, 5
-    q, k, v, _ = _make(T, H, d, d, np.float16, seed=2)
-    v[at, 1, col] = bad
-    o, hT = _forward(q, k, v, lg, 0.125)
-    ref, refT = plain.linattn(q, k, _finite(v), lg, [0, T], 0.125)
-    mag, magT = plain.absolute(plain.linattn, q, k, _finite(v), lg, [0, T], 0.125)
+@pytest.mark.parametrize("T,where", [(300, "v"), (3000, "v"), (300, "h0"), (3000, "h0")])
+def test_a_bad_value_stays_in_its_column(T, where, d, bad):
+    H, lg, col = 2, _decays(2), 5
+    q, k, v, h0 = _make(T, H, d, d, np.float16, seed=2, h0=True)
+    at = 141 if where == "v" else 0
+    if where == "v":
+        v[at, 1, col] = bad
+    else:
+        h0[0, 1, 3, col] = bad
+    o, hT = _forward(q, k, v, lg, 0.125, h0=h0)
+    a = (q, k, _finite(v), lg, [0, T], 0.125)
+    ref, refT = plain.linattn(*a, _finite(h0))
+    mag, magT = plain.absolute(plain.linattn, *a, h0=_finite(h0))
     tol, tolT = plain.tolerance(ref, mag, True, T, d), plain.sum_bound(T, d) * magT
-    assert not np.isfinite(o[at:, 1, col]).any() and not np.isfinite(hT[0, 1, :, col]).any()
+    assert not np.isfinite(o[at:at + 20, 1, col]).any()
+    assert not np.isfinite(hT[0, 1, :, col]).all()
     ref[at:, 1, col], refT[0, 1, :, col] = np.nan, np.nan      # not compared
     o[at:, 1, col] = 0.0
     plain.assert_close(o, ref, tol, "o")
