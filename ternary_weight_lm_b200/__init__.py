@@ -472,15 +472,19 @@ def bitlinear_backward(x, Wp, beta, dy, norm_w=None, eps=1e-8, A=None, gamma=Non
 
 # ------------------------------------------------------------- 8-bit projection, linear attention
 def _tensor(name, t, shape, dtypes, device, contiguous=True):
-    """Refuses a tensor that the call would misread: dtypes a tuple, shape with None for any."""
+    """Refuses a tensor that the call would misread: dtypes a tuple, shape with None for any, or the
+    number of dimensions."""
     got = t.shape
+    if (len(got) == shape if shape.__class__ is int else got == shape) and t.dtype in dtypes and \
+            t.device == device and t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if got != shape and (len(got) != len(shape) or
-                         any(s is not None and s != n for s, n in zip(shape, got))):
-        raise ValueError(f"{name}: shape {tuple(got)}, expected {shape}")
+    want = (None,) * shape if isinstance(shape, int) else shape
+    if len(got) != len(want) or any(s is not None and s != n for s, n in zip(want, got)):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {want}")
     if t.is_contiguous():
         return
     if contiguous:
@@ -511,7 +515,7 @@ def quantize_weights_int8(W, stream=None):
     """W [N, K] (fp32/fp16, CUDA, contiguous) -> (W8 int8 [N, K], wscale float32 [N])."""
     import torch
     dev = W.device
-    _tensor("W", W, (None, None), (torch.float32, torch.float16), dev)
+    _tensor("W", W, 2, (torch.float32, torch.float16), dev)
 
     def call(handle):
         W8 = torch.empty(W.shape, dtype=torch.int8, device=dev)
@@ -527,10 +531,10 @@ def int8_matmul(A, gamma, W8, wscale, out_dtype=None, out=None, stream=None):
     weights from quantize_weights_int8; fp16 unless out_dtype or out says otherwise."""
     import torch
     dev = A.device
-    _tensor("A", A, (None, None), (torch.int8,), dev)
+    _tensor("A", A, 2, (torch.int8,), dev)
     T, K = A.shape
-    _tensor("W8", W8, (None, K), (torch.int8,), dev)
     N = W8.shape[0]
+    _tensor("W8", W8, (N, K), (torch.int8,), dev)
     _tensor("gamma", gamma, (T,), (torch.float32,), dev)
     _tensor("wscale", wscale, (N,), (torch.float32,), dev)
     if out is not None:
@@ -551,10 +555,10 @@ def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws
     """RMSNorm, activation quantisation and 8-bit product of x [T, K]: y [T, N]."""
     import torch
     dev = x.device
-    _tensor("x", x, (None, None), (torch.float32, torch.float16), dev)
+    _tensor("x", x, 2, (torch.float32, torch.float16), dev)
     T, K = x.shape
-    _tensor("W8", W8, (None, K), (torch.int8,), dev)
     N = W8.shape[0]
+    _tensor("W8", W8, (N, K), (torch.int8,), dev)
     _tensor("wscale", wscale, (N,), (torch.float32,), dev)
     if norm_w is not None:
         _tensor("norm_w", norm_w, (K,), (torch.float32,), dev)
@@ -572,16 +576,16 @@ def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
     """Checks a call's tensors and describes them."""
     import torch
     dev, f = q.device, (torch.float32, torch.float16)
-    _tensor("q", q, (None, None, None), f, dev, contiguous=False)
+    _tensor("q", q, 3, f, dev, contiguous=False)
     T, H, dk = q.shape
     _tensor("k", k, (T, H, dk), (q.dtype,), dev, contiguous=False)
-    _tensor("v", v, (T, H, None), (q.dtype,), dev, contiguous=False)
-    dv = v.shape[2]
+    dv = v.shape[-1]
+    _tensor("v", v, (T, H, dv), (q.dtype,), dev, contiguous=False)
     _tensor("log_decay", log_decay, (H,), (torch.float32,), dev)
     if o is not None:
         _tensor("out", o, (T, H, dv), (q.dtype,), dev, contiguous=False)
     if cu_seqlens is not None:
-        _tensor("cu_seqlens", cu_seqlens, (None,), (torch.int32,), dev)
+        _tensor("cu_seqlens", cu_seqlens, 1, (torch.int32,), dev)
         if batch is not None and batch != cu_seqlens.numel() - 1:
             raise ValueError(f"batch {batch}, but cu_seqlens has {cu_seqlens.numel() - 1} sequences")
         batch = cu_seqlens.numel() - 1
