@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "linattn.cuh"
 #include "linattn_dev.cuh"
@@ -388,28 +389,67 @@ size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv) {
 
 void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split) {
-  // The kernel that these sizes take: tokens it handles at a time, blocks that run at once on 148
-  // SMs, and blocks for each segment, head and sweep.
+  // A model of the time, of the kernel that these sizes take.  A block handles `step` tokens at a
+  // time and `each` of them run on an SM (blocks beyond 148 each wait for the next wave); a step
+  // takes t0 + t1 n us with n blocks on an SM, a block's start and end `start` us, a pass over k and v
+  // alone about half of a whole one, and the two launches that a split adds `more` us.  Times measured on 16 heads of 128 or 64 and, in fp32, 8
+  // of 128: a step of 128 tokens with tcgen05 4.1; of 64 in the register form 3.4 alone on an SM, 8.8
+  // with four; of 16 token by token 3.2 alone, 6.1 with three.  The split is worth (us, split /
+  // whole): one prompt of 1024 28 / 36, of 4096 45 / 125, heads of 64, 4 of 512 21 / 30, fp32, one of
+  // 512 40 / 104; it is not: backward of 1024 40 / 36, heads of 64, 8 of 512 35 / 31.
   const bool half = dt == kInF16;
   const bool tc = half && dk == 128 && dv == 128;
   const bool mma = half && !tc && (dk == 64 || dk == 128) && dv % 64 == 0;
-  const int64_t step = tc ? 128 : mma ? 64 : 16;
-  const int64_t slots = 148 * (tc ? 1 : mma ? (dk == 128 ? 2 : dv % 128 == 0 ? 3 : 4)
-                                          : std::max(dk, dv) > 128 ? 2 : 4);
-  const int64_t width = tc ? 1 : mma ? dv / (dv % 128 == 0 ? 128 : 64) : (std::max(dk, dv) + 31) / 32;
-  const int64_t room = std::max<int64_t>(1, slots / (H * n_sweeps * width));   // segments
-  // Segments that fill one wave of blocks, but of at least four steps (two of 128): below that
-  // reading k and v twice and passing states through memory costs more than the blocks add.  Of
-  // a ragged batch the host knows the sum of the lengths alone: it takes half a segment more for
-  // each sequence, and the longest for three times the mean.
+  int64_t step, each, width;
+  double t0, t1, start, more;
+  if (tc) {
+    step = 128, each = 1, width = 1;
+    t0 = 4.1, t1 = 0.0, start = 3.5, more = 16.0;
+  } else if (mma) {
+    const int tile = dv % 128 == 0 ? 128 : 64;
+    const double size = dk * tile / 4096.0;
+    step = 64, each = dk == 128 ? 2 : tile == 128 ? 3 : 4, width = dv / tile;
+    t0 = 2.0 * size, t1 = 1.7 * size, start = 3.0, more = 8.0;
+  } else {
+    const int most = std::max(dk, dv);
+    const double size = most <= 64 ? 0.75 : most <= 128 ? 1.0 : 2.0;
+    step = 16, each = most > 128 ? 2 : 4, width = (most + 31) / 32;
+    t0 = 1.8 * size, t1 = 1.45 * size, start = 3.0, more = 10.0;
+  }
+  // Of a ragged batch the host knows the sum of the lengths alone: it takes the longest for three
+  // times the mean, and half a segment more for each sequence.
   const int64_t mean = (T + B - 1) / B;
   const int64_t longest = ragged ? std::min(T, 3 * mean) : mean;
-  const int64_t each = ragged ? T / std::max<int64_t>(1, room - B / 2) + 1
-                              : (mean + std::max<int64_t>(1, room / B) - 1) / std::max<int64_t>(1, room / B);
-  const int64_t L = (std::max(each, (tc ? 2 : 4) * step) + step - 1) / step * step;
-  // A step over k and v alone takes about half of a whole one; two more launches about as long as
-  // three steps (8 us against 2.5 to 4).
-  *split = longest > L && (3 * L) / (2 * step) + 3 < longest / step;
+  const double units = static_cast<double>(H) * n_sweeps * width;
+  auto time = [&](double steps, double segments) {
+    const double blocks = units * segments;
+    const double waves = std::ceil(blocks / (148.0 * each));
+    const double on = std::min<double>(each, std::max(1.0, blocks / 148.0));
+    return waves * (start + steps * (t0 + t1 * on));
+  };
+  const int64_t n = (longest + step - 1) / step, all = (T + step - 1) / step;
+  double best = time(static_cast<double>(n), static_cast<double>(B));
+  int64_t most_steps = 0;   // of a segment; none: no split
+  auto consider = [&](int64_t l) {
+    l = std::max<int64_t>(l, tc || mma ? 2 : 4);
+    if (l >= n) return;
+    const double segments = ragged ? static_cast<double>(all) / l + 0.5 * B
+                                   : static_cast<double>(B * ((n + l - 1) / l));
+    const double t = 1.5 * time(static_cast<double>(l), segments) + more;
+    if (t < best) {
+      best = t;
+      most_steps = l;
+    }
+  };
+  // segments that fill whole waves, and short ones
+  for (int waves = 1; waves <= 4; ++waves) {
+    const double room = 148.0 * each * waves / units;   // segments
+    const int64_t segments = static_cast<int64_t>(ragged ? room - 0.5 * B : room / B);
+    if (segments > 0) consider(((ragged ? all : n) + segments - 1) / segments);
+  }
+  for (int64_t l = 2; l <= 16; ++l) consider(l);
+  *split = most_steps > 0;
+  const int64_t L = most_steps * step;
   *seg_len = *split ? L : std::max<int64_t>(ragged ? T : mean, 1);
   *n_items = !*split ? B : ragged ? T / L + B : B * ((mean + L - 1) / L);
 }
