@@ -142,3 +142,13 @@ def test_another_stream_and_a_replayed_graph(T):
     graph.replay()
     torch.cuda.synchronize()
     assert np.array_equal(out.cpu().numpy(), want)
+
+
+def test_outputs_beyond_32_bits():
+    T, K, N = 70000, 16, 32000            # 2.2e9 outputs, 4.5 GB
+    A, gamma, W8, s = _inputs(T, K, N, seed=21)
+    dA, dg, dW, ds = (to_dev(x) for x in (A, gamma, W8, s))
+    y = mmf.int8_matmul(dA, dg, dW, ds)
+    for lo in (0, 67000, T - 200):
+        want = mmf.int8_matmul(dA[lo:lo + 200], dg[lo:lo + 200], dW, ds)
+        assert torch.equal(y[lo:lo + 200], want)

@@ -527,6 +527,39 @@ def test_streams_graphs_and_repeats():
     assert torch.equal(mmf.linattn_step(*tok, lg, alone), so) and torch.equal(alone, state)
 
 
+# each of the three kernels, on rows so far apart that their offsets pass 31 and 32 bits
+@pytest.mark.parametrize("d", [128, 64, 24])
+def test_offsets_beyond_32_bits(d):
+    T, H, far = 80, 2, 1 << 26            # 80 * 2^26 elements: 10 GB of fp16
+    wide = torch.empty(T * far, dtype=torch.float16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x = torch.randn(4, T, H, d, generator=g, device=DEV).half()
+    # q, k, v, do and o side by side in every row
+    rows = [wide.as_strided((T, H, d), (far, d, 1), i * H * d) for i in range(5)]
+    for r, a in zip(rows, x):
+        r.copy_(a)
+    lg = to_dev(_decays(H))
+    want = mmf.linattn_forward(*x[:3], lg)
+    mmf.linattn_forward(*rows[:3], lg, out=rows[4])
+    assert torch.equal(rows[4].contiguous(), want)
+    got = mmf.linattn_backward(*rows[:3], lg, rows[3])
+    for a, b in zip(got[:3], mmf.linattn_backward(*x[:3], lg, x[3])):
+        assert torch.equal(a, b)
+
+
+def test_a_pool_beyond_32_bits():
+    n, H, d = 8300, 16, 128               # 2.2e9 values, 8.7 GB
+    pool = torch.empty(n, H, d, d, device=DEV)
+    q, k, v, h0 = _make(2, H, d, d, np.float16, seed=1, B=2, h0=True)
+    slots = [n - 1, 0]
+    pool[slots] = to_dev(h0)
+    alone = to_dev(h0)
+    a = [to_dev(x) for x in (q, k, v, _decays(H))]
+    want = mmf.linattn_step(*a, alone)
+    got = mmf.linattn_step(*a, pool, slots=torch.tensor(slots, dtype=torch.int32, device=DEV))
+    assert torch.equal(got, want) and torch.equal(pool[slots], alone)
+
+
 def test_two_calls_at_once_with_a_workspace_each():
     T, H, d = 3000, 2, 64
     lg = to_dev(_decays(H))
