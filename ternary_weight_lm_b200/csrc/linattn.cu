@@ -29,7 +29,7 @@ namespace {
 // Per token and state element: decay, update, product with q, three fp32 operations, two rows at a
 // time (f32x2); their issue is what bounds it.  k, q and v (each v twice, as both halves of a pair)
 // come from shared memory as 16-byte broadcasts.  Measured: 1500 tokens, 8 heads of 96 x 128 in fp32,
-// 55 us, states alone 30 (the operations alone: 12 and 8); a call 88 us.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
+// 55 us, states alone 30 (the operations alone: 12 and 8); a call 89 us.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
 // through shared memory once every kTok tokens.
 constexpr int kSweepThreads = 128;
 constexpr int kTok = 16;

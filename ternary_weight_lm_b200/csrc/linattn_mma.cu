@@ -27,7 +27,7 @@
 // 0.5 us of mma.sync (555 TFLOP/s measured on this part).  Neither is reached: at 16 warps an SM the
 // issue and latency of about 1800 instructions a warp and chunk are what counts (0.4 of a scheduler's
 // slots).  Measured: 13 ragged prompts of 9001 tokens, 16 heads of 64, 49 us, their states 21, a call
-// 76 us.  Four warps with a quarter of the columns each, because a warp with 32 columns uses every
+// 78 us.  Four warps with a quarter of the columns each, because a warp with 32 columns uses every
 // operand it loads from Q, K and P twice: with 16 the loads would take as long as the products.
 #include <cuda_fp16.h>
 

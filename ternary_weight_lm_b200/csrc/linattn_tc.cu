@@ -37,7 +37,7 @@
 // memory at all of its bandwidth, and about 1800 cycles more of that for the conversions: no unit is
 // full, the hand-overs between them and the fetch of the roles' code fill the rest.  Measured: 5.0 us
 // a chunk; 32768 tokens of 16 heads in 147 us, their states alone (kState, 64 KB a chunk) in 67; whole
-// call 234 us (a register form on mma.sync: 553, two of its waves; token by token: 2991).
+// call 240 us (a register form on mma.sync: 553, two of its waves; token by token: 2991).
 //
 // Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
 // copies and MMAs in flight are drained and TMEM is freed.
