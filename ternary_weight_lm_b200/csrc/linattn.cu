@@ -393,8 +393,8 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
   // time and `each` of them run on an SM (blocks beyond 148 each wait for the next wave); a step
   // takes t0 + t1 n us with n blocks on an SM, a block's start and end `start` us, a pass over k and v
   // alone about half of a whole one, and the two launches that a split adds `more` us.  Times measured on 16 heads of 128 or 64 and, in fp32, 8
-  // of 128: a step of 128 tokens with tcgen05 4.1; of 64 in the register form 3.4 alone on an SM, 8.8
-  // with four; of 16 token by token 3.2 alone, 6.1 with three.  The split is worth (us, split /
+  // of 128: a step of 128 tokens with tcgen05 4.1; of 64 in the register form 3.4 alone on an SM, 7
+  // with three; of 16 token by token 3.2 alone, 6.1 with three.  The split is worth (us, split /
   // whole): one prompt of 1024 28 / 36, of 4096 45 / 125, heads of 64, 4 of 512 21 / 30, fp32, one of
   // 512 40 / 104; it is not: backward of 1024 40 / 36, heads of 64, 8 of 512 35 / 31.
   const bool half = dt == kInF16;
@@ -408,7 +408,7 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
   } else if (mma) {
     const int tile = dv % 128 == 0 ? 128 : 64;
     const double size = dk * tile / 4096.0;
-    step = 64, each = dk == 128 ? 2 : tile == 128 ? 3 : 4, width = dv / tile;
+    step = 64, each = dk == 128 ? 2 : 3, width = dv / tile;
     t0 = 2.0 * size, t1 = 1.7 * size, start = 3.0, more = 8.0;
   } else {
     const int most = std::max(dk, dv);

@@ -24,10 +24,11 @@
 // accumulation spans 64 tokens.
 //
 // What bounds it.  Heads of 64: 64 tokens are 32 KB, 0.7 us of an SM's share of the HBM; the products
-// 0.5 us of mma.sync (555 TFLOP/s measured on this part).  Neither is reached: at 16 warps an SM the
+// 0.5 us of mma.sync (555 TFLOP/s measured on this part).  Neither is reached: at 12 warps an SM the
 // issue and latency of about 1800 instructions a warp and chunk are what counts (0.4 of a scheduler's
-// slots).  Measured: 13 ragged prompts of 9001 tokens, 16 heads of 64, 49 us, their states 21, a call
-// 78 us.  Four warps with a quarter of the columns each, because a warp with 32 columns uses every
+// slots).  Measured: 13 ragged prompts of 9001 tokens, 16 heads of 64, 39 us, their states 21, a call
+// 69 us (with the registers for a fourth block on an SM, spilling: 50, 21 and 78; for two: as three,
+// backward a fifth slower).  Four warps with a quarter of the columns each, because a warp with 32 columns uses every
 // operand it loads from Q, K and P twice: with 16 the loads would take as long as the products.
 #include <cuda_fp16.h>
 
@@ -110,7 +111,7 @@ struct Tiles {
 };
 
 template <int DK, int DV, bool kState>
-__global__ void __launch_bounds__(kThreads, DK == 128 ? 2 : DV == 128 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, DK == 128 ? 2 : 3)
 lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   using L = Tiles<DK, DV>;
   constexpr int kStages = kState ? L::kStagesState : L::kStagesOut;
