@@ -29,7 +29,8 @@ namespace {
 // Per token and state element: decay, update, product with q, three fp32 operations, two rows at a
 // time (f32x2); their issue is what bounds it.  k, q and v (each v twice, as both halves of a pair)
 // come from shared memory as 16-byte broadcasts.  Measured: 1500 tokens, 8 heads of 96 x 128 in fp32,
-// 55 us, states alone 30 (the operations alone: 12 and 8); a call 89 us.  o is summed over the 16 row groups: four in a warp by shuffles, four warps
+// 50 us, states alone 30 (the operations alone: 12 and 8); a call 83 us (89 with the registers for a
+// fourth block on an SM).  o is summed over the 16 row groups: four in a warp by shuffles, four warps
 // through shared memory once every kTok tokens.
 constexpr int kSweepThreads = 128;
 constexpr int kTok = 16;
@@ -53,7 +54,7 @@ __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__half* p, float v) { *p = __float2half_rn(v); }
 
 template <typename T, int KR, bool kState>
-__global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 4) lin_sweep_kernel(const __grid_constant__ LinCall c) {
+__global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_kernel(const __grid_constant__ LinCall c) {
   constexpr int kRows = 16 * KR;           // padded dk
   constexpr int kVecRow = kRows / 4;       // 4-value vectors of a k or q row
   constexpr int kLoads = kTok * kVecRow / kSweepThreads;   // of k (and of q) per thread
@@ -413,7 +414,7 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
   } else {
     const int most = std::max(dk, dv);
     const double size = most <= 64 ? 0.75 : most <= 128 ? 1.0 : 2.0;
-    step = 16, each = most > 128 ? 2 : 4, width = (most + 31) / 32;
+    step = 16, each = most > 128 ? 2 : 3, width = (most + 31) / 32;
     t0 = 1.8 * size, t1 = 1.45 * size, start = 3.0, more = 10.0;
   }
   // Of a ragged batch the host knows the sum of the lengths alone: it takes the longest for three

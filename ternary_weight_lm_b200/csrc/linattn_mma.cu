@@ -28,8 +28,9 @@
 // issue and latency of about 1800 instructions a warp and chunk are what counts (0.4 of a scheduler's
 // slots).  Measured: 13 ragged prompts of 9001 tokens, 16 heads of 64, 39 us, their states 21, a call
 // 69 us (with the registers for a fourth block on an SM, spilling: 50, 21 and 78; for two: as three,
-// backward a fifth slower).  Four warps with a quarter of the columns each, because a warp with 32 columns uses every
-// operand it loads from Q, K and P twice: with 16 the loads would take as long as the products.
+// backward a fifth slower).  Four warps with a quarter of the columns each, because a warp with 32
+// columns uses every operand it loads from Q, K and P twice: with 16 the loads would take as long as
+// the products.
 #include <cuda_fp16.h>
 
 #include <algorithm>
