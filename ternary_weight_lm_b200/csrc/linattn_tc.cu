@@ -659,9 +659,12 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     // --------------------------------------------------------------------------- K to K'
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecay));
     const int r = 32 * (warp & 3) + lane;
+    // Where the group meets at a barrier (in find_exp), a warp that gave up comes along once more, so
+    // that the others are not left waiting: the loop ends for all of them there, or for each alone.
+    bool ok = true;
     for (int ch = 0; ch < chunks; ++ch) {
       const int s = ch & 1, ph = (ch >> 1) & 1;
-      const bool ok = wait(sh.bars.full[s], ph);
+      ok = ok && wait(sh.bars.full[s], ph);
       if (ok) clean_v(ch, r);
       if constexpr (kState) {
         if (!ok) break;
@@ -671,9 +674,11 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
         if (!find_exp(ch, r, 0, 2, ok, &f)) break;
         arrive(sh.bars.v[s]);
         // K is no longer read as such, nor the second part of the K' before
-        if (!wait(sh.bars.scores[s], ph) || (ch > 0 && !wait(sh.bars.upd, (ch - 1) & 1))) break;
-        decay_k(ch, r, 0, f);
-        arrive(sh.bars.k[s]);
+        ok = wait(sh.bars.scores[s], ph) && (ch == 0 || wait(sh.bars.upd, (ch - 1) & 1));
+        if (ok) {
+          decay_k(ch, r, 0, f);
+          arrive(sh.bars.k[s]);
+        }
       }
     }
   } else {
