@@ -52,13 +52,14 @@ struct Shared { Bars bars; };
 
 template <bool kState>
 void group(Meeting& meeting, int warp, int chunks, const std::set<int>& fails) {
-  constexpr int lane = 0;
+  constexpr int lane = 0, kGroup = 128;
   Shared sh;
   int waits = 0;
   auto wait = [&](int&, int) { return fails.count(waits++) == 0; };
   auto arrive = [&](int&) {};
   auto clean_v = [&](int, int) {};
   auto find_exp = [&](int, int, int, int, bool ok, float* f) { *f = 1.0f; return meeting.join(ok); };
+  auto named_bar_and = [&](int, int, bool ok) { return meeting.join(ok); };
   auto decay_k = [&](int, int, int, float) {};
   BODY
 }
