@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_con
     s_k[tid] = ld1<T>(kp + tid);
     s_q[tid] = ld1<T>(qp + tid);
   }
-  const float gamma = lin_power(lin_lg2_of(c.log_decay[h]), 1);
+  const LinDecay gamma(lin_lg2_of(c.log_decay[h]), 1);
   const int col = col0 + 4 * lane;
   const bool in = col < c.dv;
   const float4 v4 = in ? ld4<T>(vp + col) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_con
       const int r = r0 + u * kStepWarps;
       if (r < c.dk) {
         const float k = s_k[r], q = s_q[r];
-        x[u].x = fmaf(k, v4.x, gamma * x[u].x);
-        x[u].y = fmaf(k, v4.y, gamma * x[u].y);
-        x[u].z = fmaf(k, v4.z, gamma * x[u].z);
-        x[u].w = fmaf(k, v4.w, gamma * x[u].w);
+        x[u].x = gamma.next(x[u].x, k * v4.x);
+        x[u].y = gamma.next(x[u].y, k * v4.y);
+        x[u].z = gamma.next(x[u].z, k * v4.z);
+        x[u].w = gamma.next(x[u].w, k * v4.w);
         acc.x = fmaf(q, x[u].x, acc.x);
         acc.y = fmaf(q, x[u].y, acc.y);
         acc.z = fmaf(q, x[u].z, acc.z);
