@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "linattn.cuh"
 #include "linattn_dev.cuh"
@@ -26,12 +27,22 @@ namespace {
 // ------------------------------------------------------------------ token-by-token sweep
 // Block: one segment, one head, 32 columns of the state.  Thread (r, c) holds rows 4 r + 64 j ..
 // + 3 and columns 4 c .. + 3: 4 KR values in registers, in fp32 throughout (the products too).
-// Per token and state element: decay, update, product with q, three fp32 operations, two rows at a
-// time (f32x2); their issue is what bounds it.  k, q and v (each v twice, as both halves of a pair)
-// come from shared memory as 16-byte broadcasts.  Measured: 1500 tokens, 8 heads of 96 x 128 in fp32,
-// 50 us, states alone 30 (the operations alone: 12 and 8); a call 83 us (89 with the registers for a
-// fourth block on an SM).  o is summed over the 16 row groups: four in a warp by shuffles, four warps
-// through shared memory once every kTok tokens.
+// k, q and v (each v twice, as both halves of a pair) come from shared memory as 16-byte broadcasts, a
+// tile of kTok tokens at a time.
+//
+// Decay.  For a slow one (gamma^kTok at least 2^-8, which keeps the scaled sums in range) the state is
+// held over gamma^i at a tile's token i: v is scaled by gamma^-i once, outputs by gamma^i, so that a token
+// costs a state element an update and a product with q, and the state takes gamma^kTok once for
+// each tile, with the next tile's first token (LinDecay).  Fast decays, whose states last for a few tokens,
+// are taken at every token.  A product of the state with one token's decay at every token, even with the
+// two floats around it in turn, is rounded the same way as long as the state moves little: 5e-5 of a
+// state after 8192 tokens at a log decay of -1e-7, so 1e-5 at most at any (test_gpu_linattn_drift.py).
+//
+// Bound by latency: the fp32 operations, two rows at a time (f32x2), are a fourth to a third of the time,
+// the rest is each token's chain of loads from shared memory, operations and shuffles with 12 warps on an
+// SM to hide it.  Measured: 1500 tokens, 8 heads of 96 x 128 in fp32, a call 80 us (89 with the registers
+// for a fourth block on an SM).  o is summed over the 16 row groups: four in a warp by shuffles, four
+// warps through shared memory once every kTok tokens.
 constexpr int kSweepThreads = 128;
 constexpr int kTok = 16;
 constexpr int kCols = 32;
@@ -63,6 +74,7 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   __shared__ __align__(16) float s_q[kState ? 1 : kTok][kState ? 4 : kRows];
   __shared__ __align__(16) float s_v[kTok][2 * kCols];
   __shared__ float s_o[kState ? 1 : 4][kState ? 1 : kTok][kCols];
+  __shared__ float s_up[kTok + 1], s_down[kTok + 1];   // gamma^-n, gamma^n; 1 for fast decays
 
   const int slices = (max(c.sw[0].dv, c.sw[0].dk) + kCols - 1) / kCols;
   const LinSweep& w = c.sw[blockIdx.z / slices];
@@ -74,7 +86,14 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   if (!g.valid || (kState && whole)) return;
 
   const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3, warp = tid >> 5;
-  LinGamma gamma(lin_lg2(c, h));
+  const double lg2 = lin_lg2(c, h);
+  const int lag = w.backwards ? 1 : 0;   // backwards the decay acts after a token, not before it
+  const bool slow = lg2 * kTok >= -8.0;
+  const LinDecay decay(lg2, slow ? kTok : 1);
+  if (tid <= kTok) {
+    s_up[tid] = slow ? static_cast<float>(exp2(-lg2 * tid)) : 1.0f;
+    s_down[tid] = slow ? static_cast<float>(exp2(lg2 * tid)) : 1.0f;
+  }
   const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
 
@@ -119,9 +138,12 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
     rv = (p0 + tok < g.n && d < w.dv) ? ld4<T>(vp + g.token(p0 + tok) * w.v_t + d) : zero4;
   };
 
-  // forwards the decay acts before a token is added, backwards after it: held back until the next
-  float dec = w.backwards ? 1.0f : gamma.next();
+  // the decay that the state has still to take, with the next token of the full form
+  LinDecay due = decay;
+  if (slow || lag) due.whole = 1.0f, due.part = 0.0f;
   fetch(0);
+  __syncthreads();
+  const float va = w.a * s_up[tid / (kCols / 4) + 1 - lag];
   for (int64_t p0 = 0; p0 < g.n; p0 += kTok) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -130,16 +152,17 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
       if constexpr (!kState) *reinterpret_cast<float4*>(&s_q[tok][d]) = rq[i];
     }
     float4* v2 = reinterpret_cast<float4*>(&s_v[tid / (kCols / 4)][(tid % (kCols / 4)) * 8]);
-    v2[0] = make_float4(rv.x * w.a, rv.x * w.a, rv.y * w.a, rv.y * w.a);
-    v2[1] = make_float4(rv.z * w.a, rv.z * w.a, rv.w * w.a, rv.w * w.a);
+    v2[0] = make_float4(rv.x * va, rv.x * va, rv.y * va, rv.y * va);
+    v2[1] = make_float4(rv.z * va, rv.z * va, rv.w * va, rv.w * va);
     __syncthreads();
     if (p0 + kTok < g.n) fetch(p0 + kTok);
     const int nt = static_cast<int>(min(static_cast<int64_t>(kTok), g.n - p0));
-    for (int tok = 0; tok < nt; ++tok) {
-      const ulonglong2 va = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg]);
-      const ulonglong2 vb = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg + 4]);
-      const uint64_t v2[4] = {va.x, va.y, vb.x, vb.y}, dec2 = pair(dec, dec);
-      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // of the even and of the odd rows
+    auto token = [&](int tok, auto full) {
+      const ulonglong2 vlo = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg]);
+      const ulonglong2 vhi = *reinterpret_cast<const ulonglong2*>(&s_v[tok][8 * cg + 4]);
+      const uint64_t v2[4] = {vlo.x, vlo.y, vhi.x, vhi.y};
+      const uint64_t whole2 = pair(due.whole, due.whole), part2 = pair(due.part, due.part);
+      [[maybe_unused]] uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // of the even and of the odd rows
 #pragma unroll
       for (int i4 = 0; i4 < KR / 4; ++i4) {
         const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(&s_k[tok][4 * rg + 64 * i4]);
@@ -150,12 +173,15 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
           uint64_t* Sr = S[2 * i4 + z];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            Sr[j] = fma2(z ? k4.y : k4.x, v2[j], mul2(dec2, Sr[j]));
+            if constexpr (full.value)
+              Sr[j] = fma2(whole2, Sr[j], fma2(part2, Sr[j], mul2(z ? k4.y : k4.x, v2[j])));
+            else
+              Sr[j] = fma2(z ? k4.y : k4.x, v2[j], Sr[j]);
             if constexpr (!kState) sum[j] = fma2(z ? q4.y : q4.x, Sr[j], sum[j]);
           }
         }
       }
-      dec = gamma.next();
+      if constexpr (full.value) due = decay;
       if constexpr (!kState) {
         // sum over the warp's four row groups (lane bits 3 and 4); each lane ends with a column
         float acc[4];
@@ -173,6 +199,12 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
         s_o[warp][tok][4 * cg + (hi16 ? 2 : 0) + (hi8 ? 1 : 0)] =
             m + __shfl_xor_sync(0xffffffffu, y, 8);
       }
+    };
+    token(0, std::true_type{});
+    if (slow) {
+      for (int tok = 1; tok < nt; ++tok) token(tok, std::false_type{});
+    } else {
+      for (int tok = 1; tok < nt; ++tok) token(tok, std::true_type{});
     }
     __syncthreads();
     if constexpr (!kState) {
@@ -182,14 +214,16 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
         const int x = tid + i * kSweepThreads, tok = x / kCols, cc = x % kCols;
         if (tok < nt && col0 + cc < w.dv) {
           const float y = (s_o[0][tok][cc] + s_o[1][tok][cc]) + (s_o[2][tok][cc] + s_o[3][tok][cc]);
-          st1(op + g.token(p0 + tok) * w.o_t + col0 + cc, y * w.b);
+          st1(op + g.token(p0 + tok) * w.o_t + col0 + cc, y * (w.b * s_down[tok + 1 - lag]));
         }
       }
     }
   }
 
   if (!kState && !(whole && w.sT)) return;
-  const float end = (w.backwards && g.n > 0) ? dec : 1.0f;
+  // the decay still due: of the last tile's tokens, of the last token backwards, or none
+  const int64_t left = g.n == 0 ? 0 : slow ? (g.n - 1) % kTok + 1 : lag;
+  const LinDecay end(lg2, left);
 #pragma unroll
   for (int i = 0; i < KR; ++i)
 #pragma unroll
@@ -197,7 +231,7 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
       const int row = row_of(i), col = col0 + 4 * cg + j;
       if (row >= w.dk || col >= w.dv) continue;
       const float2 p = unpair(S[i / 2][j]);
-      const float x = ((i & 1) ? p.y : p.x) * end;
+      const float x = left > 0 ? end.next((i & 1) ? p.y : p.x, 0.0f) : (i & 1) ? p.y : p.x;
       if (kState)
         seg[static_cast<size_t>(row) * w.dv + col] = x;
       else

@@ -56,6 +56,7 @@ __device__ __forceinline__ float lin_power(double lg2, int64_t n) {
 // part x alone rounded into x, decays next to 1 would come to nothing.
 struct LinDecay {
   float whole, part;
+  LinDecay() = default;
   __device__ __forceinline__ LinDecay(double lg2, int64_t n) {
     const double g = n == 0 ? 1.0 : exp2(lg2 * static_cast<double>(n));
     whole = g >= 0.5 ? 1.0f : 0.0f;
@@ -72,26 +73,6 @@ struct LinDecay {
 __device__ __forceinline__ float lin_nan_if_inf(float x) {
   return isinf(x) ? __int_as_float(0x7fffffff) : x;
 }
-
-// A head's decay token by token.  gamma rounded to float is off by up to 2^-25, the same way every
-// time, which 512 tokens would raise to 10^-5 of a state.  So the two floats around gamma take
-// turns, in proportion: their products stay within one rounding of gamma's powers.
-struct LinGamma {
-  float lo, hi, share, sum;
-  __device__ __forceinline__ explicit LinGamma(double lg2) {
-    const double g = exp2(lg2);
-    lo = __double2float_rd(g);
-    hi = __double2float_ru(g);
-    share = hi > lo ? static_cast<float>((g - lo) / (static_cast<double>(hi) - lo)) : 0.0f;
-    sum = 0.5f;
-  }
-  __device__ __forceinline__ float next() {
-    sum += share;
-    const bool up = sum >= 1.0f;
-    sum = up ? sum - 1.0f : sum;
-    return up ? hi : lo;
-  }
-};
 
 struct LinSeg {
   bool valid;      // false: the item is past the last segment

@@ -43,3 +43,39 @@ def test_thousands_of_steps(dt):
         mmf.linattn_step(dq[t:t + 1], dk[t:t + 1], dv[t:t + 1], lg, state)
     torch.cuda.synchronize()
     _check(state[0].cpu().numpy(), _states(q, k, v, LG, h0), np.sqrt(3 * n) * plain.U32)
+
+
+def _backward_states(q, do, lg, scale, dhT):
+    """The gradient of the state before the first token (64 bits)."""
+    g = plain.gammas(lg)[:, None, None]
+    U = dhT.astype(np.float64)
+    for t in range(q.shape[0] - 1, -1, -1):
+        U = g * (U + scale * q[t].astype(np.float64)[:, :, None] * do[t].astype(np.float64)[:, None, :])
+    return U
+
+
+# In one segment (heads enough to fill the GPU; they share their rows) and in many.  The token-by-token
+# form rounds a state twice for each token, and what is added once.
+@pytest.mark.parametrize("dt,d,T,H,split", [
+    (np.float32, 64, 8192, 444, False), (np.float32, 64, 8192, 8, True)])
+def test_long_prompts(dt, d, T, H, split):
+    n = len(LG)
+    rng = np.random.default_rng(T + d + H)
+    x = [rng.normal(size=(T, d)).astype(dt) for _ in range(4)]
+    h0, dhT = ((rng.normal(size=(n, d, d)) * 100).astype(np.float32) for _ in range(2))
+    q, k, v, do = (to_dev(a)[:, None].expand(T, H, d) for a in x)
+    do = do.contiguous()
+    lg = to_dev(np.resize(LG, H))
+    s0, sT = (torch.zeros(1, H, d, d, device=DEV) for _ in range(2))
+    s0[0, :n], sT[0, :n] = to_dev(h0), to_dev(dhT)
+    need = mmf.mmf_linattn_workspace_bytes(mmf._linattn(q, k, v, lg, None, None, None, None))
+    assert (need > 0) == split
+    hT = torch.empty_like(s0)
+    mmf.linattn_forward(q, k, v, lg, h0=s0, hT=hT)
+    dh0 = mmf.linattn_backward(q, k, v, lg, do, scale=0.1, dhT=sT, want_dh0=True)[3]
+    torch.cuda.synchronize()
+    assert mmf.mmf_get_device_status() == 0
+    bound = np.sqrt(3 * T) * plain.U32
+    a = [np.broadcast_to(y[:, None], (T, n, d)) for y in x]
+    _check(hT[0, :n].cpu().numpy(), _states(*a[:3], LG, h0), bound)
+    _check(dh0[0, :n].cpu().numpy(), _backward_states(a[0], a[3], LG, 0.1, dhT), bound)
