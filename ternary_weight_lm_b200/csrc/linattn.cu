@@ -252,8 +252,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
   const int64_t n = lin_segments(c, b, &first, &len);   // whole warps
   if (n < 2 || e >= w.dk * w.dv) return;
   const double lg2 = lin_lg2(c, h);
-  const float gl = lin_power(lg2, c.seg_len);
-  const float glast = lin_power(lg2, max(len - (n - 1) * c.seg_len, static_cast<int64_t>(0)));
+  const LinDecay gl(lg2, c.seg_len), glast(lg2, max(len - (n - 1) * c.seg_len, static_cast<int64_t>(0)));
   const int i = e / w.dv, j = e % w.dv;
   const size_t state = static_cast<size_t>(w.dk) * w.dv;
   const size_t at = (static_cast<size_t>(b) * c.H + h) * state + static_cast<size_t>(i) * w.s_key +
@@ -279,11 +278,11 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
         if (x + kAhead < n) own[u] = *reinterpret_cast<const float4*>(slot + kAhead * step);
         *reinterpret_cast<float4*>(slot) = S;
         slot += step;
-        const float f = x + 1 < n ? gl : glast;
-        S.x = fmaf(f, S.x, o.x);
-        S.y = fmaf(f, S.y, o.y);
-        S.z = fmaf(f, S.z, o.z);
-        S.w = fmaf(f, S.w, o.w);
+        const LinDecay& f = x + 1 < n ? gl : glast;
+        S.x = f.next(S.x, o.x);
+        S.y = f.next(S.y, o.y);
+        S.z = f.next(S.z, o.z);
+        S.w = f.next(S.w, o.w);
       }
     }
   }

@@ -20,7 +20,7 @@
 // that is rounded to 2^-11 itself.  The decayed V is carried as two fp16 parts, 22 bits: the state
 // is an fp32 output, and a third rounding would cost more than it saves (one part alone, measured:
 // error against 64 bits 0.00035 instead of 0.00029, the output's own rounding being 0.00021).  All
-// sums are fp32; the state adds a chunk's product by one fp32 operation, so the tensor cores' own
+// sums are fp32; the state takes a chunk's product in one fp32 rounding, so the tensor cores' own
 // accumulation spans 64 tokens.
 //
 // What bounds it.  Heads of 64: 64 tokens are 32 KB, 0.7 us of an SM's share of the HBM; the products
@@ -124,6 +124,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float s_pow[kC + 1];     // gamma^0 .. gamma^64
   __shared__ int s_exp[kC];           // exponent of each row of P
+  __shared__ LinDecay s_decay[2];     // of a whole chunk, of the last one
 
   const LinSweep& w = c.sw[sweep0 + blockIdx.z / tiles];
   const int h = blockIdx.y;
@@ -136,6 +137,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   const int lag = w.backwards ? 1 : 0;
   const double lg2 = lin_lg2(c, h);
   if (tid <= kC) s_pow[tid] = lin_power(lg2, tid);
+  if (tid < 2) s_decay[tid] = LinDecay(lg2, tid == 0 || g.n % kC == 0 ? kC : g.n % kC);
 
   const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
@@ -464,7 +466,8 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             lo[kk][m][2 * z + y] = *reinterpret_cast<const uint32_t*>(&l2);
           }
       }
-    const float decay = s_pow[n], back = pow2(-ev);
+    const LinDecay decay = s_decay[n < kC];
+    const float back = pow2(-ev);
     top = 0.0f;
     constexpr int NG = 4;             // column tiles of S^T at a time
 #pragma unroll
@@ -500,7 +503,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float& y = S[m][n0 + x][e];
-            y = fmaf(decay, y, D[m][x][e] * back);
+            y = decay.next(y, D[m][x][e] * back);
             if constexpr (!kState) {
               if (e & 1) top = max3_abs(top, S[m][n0 + x][e - 1], y);
             }

@@ -23,7 +23,7 @@
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
 // K' scaled by powers of two (a row's, the state's, the chunk's) before they are rounded.  The
-// state adds a chunk's product by one fp32 operation.
+// state takes a chunk's product in one fp32 rounding.
 //
 // A v that is not finite would reach earlier tokens through P V as 0 times infinity.  Such values
 // are replaced by zero on arrival and their place is noted: from that token on the column's
@@ -238,6 +238,7 @@ struct Bars {
 struct Shared {
   Bars bars;
   float pow[kC + 4];        // gamma^0 .. gamma^128
+  LinDecay decay[2];        // of a whole chunk, of the last one
   float diag[64];           // diag[32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i
   alignas(16) float col[32];   // gamma^(31-j) forwards, gamma^j backwards
   float red_k[2][8], red_w[2][8], top_k[2][8], red_s[4];   // of each warp (a panel's four)
@@ -307,6 +308,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int d = back ? tid - 32 : 32 - tid;
     sh.diag[tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
   }
+  if (tid < 2) sh.decay[tid] = LinDecay(lin_lg2(c, h), tid == 0 || g.n % kC == 0 ? kC : g.n % kC);
   if (tid < 32) {
     sh.col[tid] = lin_power(lin_lg2(c, h), back ? tid : 31 - tid);
   }
@@ -614,8 +616,10 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       const bool w2 = wait(sh.bars.upd, ch & 1);
       if (w2) {
         tc_fence_after();
-        const float decay = sh.pow[tokens(ch)], f = pow2(-sh.exp_k[ch & 3]);
-        const uint64_t decay2 = pair(decay, decay), f2 = pair(f, f);
+        const LinDecay decay = sh.decay[tokens(ch) < kC];
+        const float f = pow2(-sh.exp_k[ch & 3]);
+        const uint64_t whole2 = pair(decay.whole, decay.whole), part2 = pair(decay.part, decay.part);
+        const uint64_t f2 = pair(f, f);
         top[0] = top[1] = top[2] = top[3] = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -625,7 +629,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             uint64_t& x = S[16 * b + i];
-            x = fma2(decay2, x, mul2(pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), f2));
+            x = fma2(whole2, x, fma2(part2, x, mul2(pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), f2)));
             if constexpr (!kState) {
               const float2 y = unpair(x);
               top[i & 3] = max3_abs(top[i & 3], y.x, y.y);
