@@ -314,7 +314,8 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  *
  * q, k [T x H x dk], v, o [T x H x dv], all of dtype dt, the last dimension contiguous; *_t and
  * *_h are the strides of a token and of a head in elements, multiples of 16 bytes, not negative
- * (0 shares a row between heads or tokens; not for o).  Tokens are packed: with cu_seqlens
+ * (0 shares a row between heads or tokens; not for o, whose rows have no value in common, nor for
+ * dout).  Tokens are packed: with cu_seqlens
  * ([B + 1] int32 on the device, ascending, within 0..T) sequence b has the tokens
  * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
  * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are neither read nor

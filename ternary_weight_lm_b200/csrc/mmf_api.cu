@@ -569,17 +569,24 @@ mmf_status check_strides(int64_t t, int64_t h, int dt) {
   return t % v == 0 && h % v == 0 ? MMF_OK : MMF_ERR_ALIGNMENT;
 }
 
-// Strides of an output: no two rows of d values in one place.
-mmf_status check_out_strides(int64_t t, int64_t h, int64_t nt, int64_t nh, int64_t d, int dt) {
+// Strides of o or dout: rows of d values next to one another, and where they are written no two rows
+// of different tokens and heads with a value in common (all heads of a token lie before the next
+// token's, or all tokens of a head before the next head's).
+mmf_status check_out_strides(int64_t t, int64_t h, int64_t nt, int64_t nh, int64_t d, int dt,
+                             bool written) {
   mmf_status st = check_strides(t, h, dt);
   if (st != MMF_OK) return st;
   if ((nt > 1 && t < d) || (nh > 1 && h < d)) return MMF_ERR_INVALID_ARG;
+  using wide = __int128;   // a stride times a count can pass 64 bits
+  if (written && nt > 1 && nh > 1 && static_cast<wide>(t) < static_cast<wide>(nh - 1) * h + d &&
+      static_cast<wide>(h) < static_cast<wide>(nt - 1) * t + d)
+    return MMF_ERR_INVALID_ARG;
   return MMF_OK;
 }
 
 // Checks a descriptor and copies it to *n, with the stride of a dimension of one, which says
-// nothing, as a contiguous tensor has it.
-mmf_status check_desc(const mmf_linattn_desc* d, mmf_linattn_desc* n) {
+// nothing, as a contiguous tensor has it.  o_written: o's strides are an output's.
+mmf_status check_desc(const mmf_linattn_desc* d, mmf_linattn_desc* n, bool o_written) {
   if (!d || !d->log_decay || check_dtype(d->dt) != MMF_OK) return MMF_ERR_INVALID_ARG;
   if (!(d->scale == d->scale) || d->scale - d->scale != 0.0f) return MMF_ERR_INVALID_ARG;
   mmf_status st;
@@ -600,7 +607,7 @@ mmf_status check_desc(const mmf_linattn_desc* d, mmf_linattn_desc* n) {
   if ((st = check_strides(n->q_t, n->q_h, d->dt)) != MMF_OK ||
       (st = check_strides(n->k_t, n->k_h, d->dt)) != MMF_OK ||
       (st = check_strides(n->v_t, n->v_h, d->dt)) != MMF_OK ||
-      (st = check_out_strides(n->o_t, n->o_h, d->T, d->H, d->dv, d->dt)) != MMF_OK)
+      (st = check_out_strides(n->o_t, n->o_h, d->T, d->H, d->dv, d->dt, o_written)) != MMF_OK)
     return st;
   return MMF_OK;
 }
@@ -653,7 +660,7 @@ MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* desc, const vo
   if (!q || !k || !v || !o) return MMF_ERR_INVALID_ARG;
   mmf_linattn_desc checked;
   const mmf_linattn_desc* d = &checked;
-  mmf_status st = check_desc(desc, &checked);
+  mmf_status st = check_desc(desc, &checked, true);
   if (st != MMF_OK) return st;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
       (h0 && !aligned(h0, 16)) || (hT && !aligned(hT, 16)))
@@ -694,7 +701,7 @@ MMF_EXPORT mmf_status mmf_linattn_backward(const mmf_linattn_desc* desc, const v
   if (dh0 && (dh0 == dhT || dh0 == h0)) return MMF_ERR_INVALID_ARG;
   mmf_linattn_desc checked;
   const mmf_linattn_desc* d = &checked;
-  mmf_status st = check_desc(desc, &checked);
+  mmf_status st = check_desc(desc, &checked, false);
   if (st != MMF_OK) return st;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dout, 16) ||
       !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || (h0 && !aligned(h0, 16)) ||
@@ -780,7 +787,7 @@ MMF_EXPORT mmf_status mmf_linattn_step(const mmf_linattn_desc* desc, const void*
   if (!q || !k || !v || !o || !state) return MMF_ERR_INVALID_ARG;
   mmf_linattn_desc checked;
   const mmf_linattn_desc* d = &checked;
-  mmf_status st = check_desc(desc, &checked);
+  mmf_status st = check_desc(desc, &checked, true);
   if (st != MMF_OK) return st;
   if (d->cu_seqlens || d->T != d->B) return MMF_ERR_INVALID_ARG;
   if (slots ? (n_slots < 1 || n_slots > kMaxBatch) : n_slots != 0) return MMF_ERR_INVALID_ARG;

@@ -1,0 +1,40 @@
+"""Host-side checks of the linear attention's descriptor and of what the binding passes on."""
+import ctypes
+
+import pytest
+import torch
+
+import ternary_weight_lm_b200 as mmf
+from test_operators_host import A16, CUDA, INVALID, desc
+
+
+# rows of o in one place: strides that are each at least a row, and are not enough together
+@pytest.mark.parametrize("kw", [
+    dict(o_t=128, o_h=128), dict(o_t=128, o_h=192), dict(o_t=384, o_h=128), dict(o_t=504, o_h=128),
+    dict(o_t=128, o_h=128 * 598), dict(o_t=136, o_h=136),
+    # the products pass 64 bits
+    dict(o_t=1 << 61, o_h=1 << 61), dict(T=16777215, B=3, o_t=1 << 60, o_h=(1 << 60) + 8),
+])
+def test_rows_of_an_output_in_one_place_are_refused(kw):
+    L, r = mmf.lib(), ctypes.byref(desc(**kw))
+    assert L.mmf_linattn_forward(r, A16, A16, A16, None, A16, None, A16, 1 << 40, None) == INVALID
+    T = kw.get("T", 600)
+    r = ctypes.byref(desc(**{**kw, "T": min(T, 600), "B": min(T, 600)}))
+    assert L.mmf_linattn_step(r, A16, A16, A16, A16, A16, None, 0, None) == INVALID
+    if torch.cuda.is_available():
+        return                   # what follows is not refused, and the addresses are not real
+    # dout is only read
+    assert L.mmf_linattn_backward(r, A16, A16, A16, A16, None, None, A16, A16, A16, None, A16,
+                                  1 << 40, None) == CUDA
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(o_t=128, o_h=128 * 600), dict(o_t=136, o_h=136 * 600), dict(o_t=552, o_h=136),
+    dict(T=1, B=1, o_t=8, o_h=128), dict(H=1, o_t=128, o_h=8), dict(o_t=512, o_h=128),
+])
+def test_rows_of_an_output_apart_are_taken(kw):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    L, r = mmf.lib(), ctypes.byref(desc(**kw))
+    assert L.mmf_linattn_forward(r, A16, A16, A16, None, A16, None, A16, 1 << 40, None) == CUDA
+
