@@ -339,7 +339,8 @@ typedef struct {
 } mmf_linattn_desc;
 
 /* Workspace bytes of the forward and of the backward (0 where none is needed, and for a
- * descriptor outside the limits). */
+ * descriptor outside the limits).  Enough for a call with the descriptor's strides and for one with
+ * packed rows: which kernel runs, and so how many segments there are, can depend on them. */
 size_t mmf_linattn_workspace_bytes(const mmf_linattn_desc* d);
 size_t mmf_linattn_backward_workspace_bytes(const mmf_linattn_desc* d);
 

@@ -421,9 +421,24 @@ size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv) {
   return (static_cast<size_t>(n_items) * H * dk * dv * 4 + 255) / 256 * 256;
 }
 
-void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
+LinForm lin_form(int H, int dk, int dv, int dt, int n_sweeps, const int64_t (*strides)[2]) {
+  if (dt != kInF16) return kLinTokens;
+  if (dk == 128 && dv == 128) {
+    // tensor maps: none for a row that every token shares, columns counted in 31 bits, rows in 40
+    bool maps = true;
+    for (int i = 0; i < (n_sweeps > 1 ? 4 : 3); ++i)
+      maps &= strides[i][0] > 0 && strides[i][0] < (1ll << 38) &&
+              (H == 1 || strides[i][1] <= (0x7fffffff - 128) / (H - 1));
+    if (maps) return kLinTc;
+  }
+  // a sweep's dk is 64 or 128, its dv a multiple of 64; the backward's have both orders
+  auto keys = [](int d) { return d == 64 || d == 128; };
+  return keys(dk) && (n_sweeps > 1 ? keys(dv) : dv % 64 == 0) ? kLinMma : kLinTokens;
+}
+
+void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, LinForm form, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split) {
-  // A model of the time, of the kernel that these sizes take.  A block handles `step` tokens at a
+  // A model of the time, of the kernel that the call takes.  A block handles `step` tokens at a
   // time and `each` of them run on an SM (blocks beyond 148 each wait for the next wave); a step
   // takes t0 + t1 n us with n blocks on an SM, a block's start and end `start` us, a pass over k and v
   // alone about half of a whole one, and the two launches that a split adds `more` us.  Times measured on 16 heads of 128 or 64 and, in fp32, 8
@@ -431,9 +446,7 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
   // with three; of 16 token by token 3.2 alone, 6.1 with three.  The split is worth (us, split /
   // whole): one prompt of 1024 28 / 36, of 4096 45 / 125, heads of 64, 4 of 512 21 / 30, fp32, one of
   // 512 40 / 104; it is not: backward of 1024 40 / 36, heads of 64, 8 of 512 35 / 31.
-  const bool half = dt == kInF16;
-  const bool tc = half && dk == 128 && dv == 128;
-  const bool mma = half && !tc && (dk == 64 || dk == 128) && dv % 64 == 0;
+  const bool tc = form == kLinTc, mma = form == kLinMma;
   int64_t step, each, width;
   double t0, t1, start, more;
   if (tc) {
@@ -489,8 +502,8 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, 
 }
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s) {
-  if (lin_tc_supported(c)) return launch_lin_tc(c, s);
-  if (lin_mma_supported(c)) return launch_lin_mma(c, s);
+  if (c.form == kLinTc) return launch_lin_tc(c, s);
+  if (c.form == kLinMma) return launch_lin_mma(c, s);
   return c.dt == kInF16 ? sweeps_of<__half>(c, s) : sweeps_of<float>(c, s);
 }
 

@@ -29,6 +29,10 @@ struct LinSweep {
 
 constexpr int kMaxSweeps = 3;
 
+// The kernels of a sweep: token by token (every type and size), chunks of 64 tokens on mma.sync, chunks
+// of 128 on tcgen05.
+enum LinForm { kLinTokens, kLinMma, kLinTc };
+
 // A call.  Sequence b has the tokens [cu[b], cu[b + 1]) or, without cu, [b T / B, (b + 1) T / B).
 // Work items: every sequence is cut into segments of `seg_len` tokens in the sweep's order (the
 // last one is shorter); item x of n_items names a sequence and a segment, items past the last are
@@ -36,6 +40,7 @@ constexpr int kMaxSweeps = 3;
 struct LinCall {
   LinSweep sw[kMaxSweeps];
   int n_sweeps;
+  LinForm form;            // of every sweep
   int dt;                  // InDType of q, k, v, o
   int64_t T;
   int B;
@@ -48,22 +53,21 @@ struct LinCall {
   unsigned* status;
 };
 
-// Segment length for a call of these sizes and type (a function of them alone), the number of
-// items and whether the sequences are split.
-void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, int dt, int n_sweeps,
+// Which form a call of these sizes, type and strides takes (token and head of q, k, v and, backwards,
+// of the outputs' gradient).
+LinForm lin_form(int H, int dk, int dv, int dt, int n_sweeps, const int64_t (*strides)[2]);
+// Segment length for a call of these sizes and form (a function of them alone), the number of items
+// and whether the sequences are split.
+void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, LinForm form, int n_sweeps,
               int64_t* seg_len, int64_t* n_items, int* split);
 size_t lin_seg_bytes(int64_t n_items, int H, int dk, int dv);
 
 cudaError_t launch_linattn(const LinCall& c, cudaStream_t s);
 
-// The same on the tensor cores: fp16, every dk 64 or 128, every dv a multiple of 64.
-bool lin_mma_supported(const LinCall& c);
 cudaError_t launch_lin_mma(const LinCall& c, cudaStream_t s);
 // The second pass of a split: every segment's start state from the segments' own contributions.
 cudaError_t launch_lin_join(const LinCall& c, cudaStream_t s);
 
-// And with tcgen05: fp16 heads of 128 x 128.
-bool lin_tc_supported(const LinCall& c);
 cudaError_t launch_lin_tc(const LinCall& c, cudaStream_t s);
 
 // One token of each sequence: state [rows x H x dk x dv] updated in place, o = scale S^T q.

@@ -584,13 +584,6 @@ cudaError_t launch_all(const LinCall& c, bool state, cudaStream_t s) {
 
 }  // namespace
 
-bool lin_mma_supported(const LinCall& c) {
-  if (c.dt != kInF16) return false;
-  for (int i = 0; i < c.n_sweeps; ++i)
-    if ((c.sw[i].dk != 64 && c.sw[i].dk != 128) || c.sw[i].dv % 64 != 0) return false;
-  return true;
-}
-
 cudaError_t launch_lin_mma(const LinCall& c, cudaStream_t s) {
   if (c.split) {
     cudaError_t e = launch_all(c, true, s);

@@ -850,19 +850,6 @@ bool map_heads(CUtensorMap* m, const void* p, int64_t T, int H, int64_t t_stride
 
 }  // namespace
 
-bool lin_tc_supported(const LinCall& c) {
-  if (c.dt != kInF16) return false;
-  for (int i = 0; i < c.n_sweeps; ++i) {
-    const LinSweep& w = c.sw[i];
-    if (w.dk != kD || w.dv != kD) return false;
-    const int64_t st[3][2] = {{w.q_t, w.q_h}, {w.k_t, w.k_h}, {w.v_t, w.v_h}};
-    for (const auto& x : st)
-      // a row that every token shares has no tensor map, and columns are counted in 31 bits
-      if (x[0] == 0 || x[0] >= (1ll << 38) || (c.H - 1) * x[1] + kD > 0x7fffffff) return false;
-  }
-  return true;
-}
-
 cudaError_t launch_lin_tc(const LinCall& c, cudaStream_t s) {
   LinMaps maps;
   for (int i = 0; i < c.n_sweeps; ++i) {

@@ -3,6 +3,7 @@
 // a rejected call never touches the device.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -620,7 +621,9 @@ void lin_call(const mmf_linattn_desc* d, int n_sweeps, LinCall* c) {
   c->H = d->H;
   c->cu = d->cu_seqlens;
   c->log_decay = d->log_decay;
-  lin_plan(d->T, d->B, d->cu_seqlens != nullptr, d->H, d->dk, d->dv, c->dt, n_sweeps, &c->seg_len,
+  const int64_t strides[4][2] = {{d->q_t, d->q_h}, {d->k_t, d->k_h}, {d->v_t, d->v_h}, {d->o_t, d->o_h}};
+  c->form = lin_form(d->H, d->dk, d->dv, c->dt, n_sweeps, strides);
+  lin_plan(d->T, d->B, d->cu_seqlens != nullptr, d->H, d->dk, d->dv, c->form, n_sweeps, &c->seg_len,
            &c->n_items, &c->split);
 }
 
@@ -630,6 +633,18 @@ size_t lin_ws_bytes(const mmf_linattn_desc* d, int n_sweeps) {
   LinCall c = {};
   lin_call(d, n_sweeps, &c);
   return c.split ? n_sweeps * lin_seg_bytes(c.n_items, d->H, d->dk, d->dv) : 0;
+}
+
+// What a caller is told: enough for the call with these strides and for the one with packed rows (its
+// kernel can be another), since a caller may ask before it has set the strides.
+size_t lin_ws_query(const mmf_linattn_desc* d, int n_sweeps) {
+  if (!d) return 0;
+  mmf_linattn_desc p = *d;
+  p.q_t = p.k_t = static_cast<int64_t>(d->H) * d->dk;
+  p.v_t = p.o_t = static_cast<int64_t>(d->H) * d->dv;
+  p.q_h = p.k_h = d->dk;
+  p.v_h = p.o_h = d->dv;
+  return std::max(lin_ws_bytes(d, n_sweeps), lin_ws_bytes(&p, n_sweeps));
 }
 
 mmf_status lin_workspace(const mmf_linattn_desc* d, void* ws, size_t ws_bytes, LinCall* c) {
@@ -647,11 +662,11 @@ mmf_status lin_workspace(const mmf_linattn_desc* d, void* ws, size_t ws_bytes, L
 }  // namespace
 
 MMF_EXPORT size_t mmf_linattn_workspace_bytes(const mmf_linattn_desc* d) {
-  return lin_ws_bytes(d, 1);
+  return lin_ws_query(d, 1);
 }
 
 MMF_EXPORT size_t mmf_linattn_backward_workspace_bytes(const mmf_linattn_desc* d) {
-  return lin_ws_bytes(d, 3);
+  return lin_ws_query(d, 3);
 }
 
 MMF_EXPORT mmf_status mmf_linattn_forward(const mmf_linattn_desc* desc, const void* q, const void* k,

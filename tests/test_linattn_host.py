@@ -38,3 +38,22 @@ def test_rows_of_an_output_apart_are_taken(kw):
     L, r = mmf.lib(), ctypes.byref(desc(**kw))
     assert L.mmf_linattn_forward(r, A16, A16, A16, None, A16, None, A16, 1 << 40, None) == CUDA
 
+
+
+# Segments are chosen for the kernel that runs.  The workspace has a state for each of them.
+def test_segments_are_those_of_the_kernel_that_runs():
+    need, grad = mmf.mmf_linattn_workspace_bytes, mmf.mmf_linattn_backward_workspace_bytes
+    one = dict(T=16384, B=1, H=4)
+    # backward, the tensor cores take heads of 64 and 128 only: other sizes run as in fp32
+    for dk, dv in ((64, 192), (64, 256), (128, 192), (96, 128)):
+        kw = dict(one, dk=dk, dv=dv)
+        assert grad(desc(**kw)) == grad(desc(**kw, dt=0)) > 0
+    assert need(desc(**one, dk=64, dv=192)) != need(desc(**one, dk=64, dv=192, dt=0)) > 0
+    # heads of 128: a row that all tokens share has no tensor map, whichever tensor has it
+    kw = dict(one, dk=128, dv=128)
+    shared = {need(desc(**kw, **{n: 0})) for n in ("q_t", "k_t", "v_t")}
+    assert len(shared) == 1 and need(desc(**kw)) not in shared and 0 not in shared
+    shared = {grad(desc(**kw, **{n: 0})) for n in ("q_t", "k_t", "v_t")}
+    assert len(shared) == 1 and grad(desc(**kw)) not in shared and 0 not in shared
+    # heads further apart than a tensor map's columns go
+    assert need(desc(**kw, k_h=1 << 30)) == need(desc(**kw, q_h=1 << 62)) == need(desc(**kw, q_t=0))
