@@ -318,8 +318,8 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  * dout).  Tokens are packed: with cu_seqlens
  * ([B + 1] int32 on the device, ascending, within 0..T) sequence b has the tokens
  * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
- * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are neither read nor
- * written.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is
+ * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are not read, and not
+ * written either unless clear_outside asks for zeros in their rows of o, dq, dk and dv.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is
  * touched, the outputs are then unspecified and mmf_get_device_status returns MMF_ERR_PLAN.
  * Shapes: 1 <= T <= 16777216, 1 <= B <= 2^20, 1 <= H <= 4096, dk and dv multiples of 8 from 8 to
  * 256.  Pointers to matrices are 16-byte aligned, ws is 256-byte aligned (NULL with ws_bytes 0
@@ -334,6 +334,7 @@ typedef struct {
   int32_t H, dk, dv;
   mmf_dtype dt;                 /* of q, k, v, o and of dq, dk, dv */
   float scale;
+  int32_t clear_outside;        /* not 0: outputs get zeros for tokens outside the sequences */
   const float* log_decay;       /* device, [H] */
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
 } mmf_linattn_desc;

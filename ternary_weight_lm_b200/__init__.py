@@ -65,7 +65,8 @@ class LinattnDesc(ctypes.Structure):
     """Mirror of the C struct mmf_linattn_desc (sizes and strides of a linear attention call)."""
     _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
                 ("H", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
-                ("dt", ctypes.c_int), ("scale", ctypes.c_float), ("log_decay", ctypes.c_void_p),
+                ("dt", ctypes.c_int), ("scale", ctypes.c_float), ("clear_outside", ctypes.c_int32),
+                ("log_decay", ctypes.c_void_p),
                 ("q_t", ctypes.c_int64), ("q_h", ctypes.c_int64), ("k_t", ctypes.c_int64),
                 ("k_h", ctypes.c_int64), ("v_t", ctypes.c_int64), ("v_h", ctypes.c_int64),
                 ("o_t", ctypes.c_int64), ("o_h", ctypes.c_int64)]
@@ -572,8 +573,8 @@ def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws
     return _on(x, stream, call)
 
 
-def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
-    """Checks a call's tensors and describes them."""
+def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch, clear=False):
+    """Checks a call's tensors and describes them; clear: zeros for tokens outside the sequences."""
     import torch
     dev, f = q.device, (torch.float32, torch.float16)
     _tensor("q", q, 3, f, dev, contiguous=False)
@@ -591,7 +592,7 @@ def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch):
         batch = cu_seqlens.numel() - 1
     return LinattnDesc(
         T, 1 if batch is None else batch, _ptr(cu_seqlens), H, dk, dv, _dt(q),
-        dk ** -0.5 if scale is None else scale, _ptr(log_decay), *q.stride()[:2],
+        dk ** -0.5 if scale is None else scale, clear, _ptr(log_decay), *q.stride()[:2],
         *k.stride()[:2], *v.stride()[:2], *((H * dv, dv) if o is None else o.stride()[:2]))
 
 
@@ -614,10 +615,10 @@ def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None,
     strides of whole 16 bytes; log_decay [H] fp32, at most 0; scale: dk ** -0.5 unless given.
     cu_seqlens [B + 1] int32 (device), or batch equal sequences (1 unless given).  h0, hT
     [B, H, dk, dv] fp32: states before (zero unless given) and after (written if given; may be
-    h0)."""
+    h0).  Rows of tokens outside the sequences are zero, or left as they were in a given out."""
     import torch
     dev = q.device
-    d = _linattn(q, k, v, log_decay, out, scale, cu_seqlens, batch)
+    d = _linattn(q, k, v, log_decay, out, scale, cu_seqlens, batch, out is None)
     _linattn_states(d, dev, h0=h0, hT=hT)
 
     def call(handle):
@@ -659,10 +660,10 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batc
     """Gradients of linattn_forward: ``(dq, dk, dv, dh0)`` (dh0 None unless asked for).
 
     dout [T, H, dv]: the gradient of o; dhT: that of hT (none unless given).  Rows of tokens
-    outside the sequences are not written."""
+    outside the sequences are zero."""
     import torch
     dev = q.device
-    d = _linattn(q, k, v, log_decay, dout, scale, cu_seqlens, batch)
+    d = _linattn(q, k, v, log_decay, dout, scale, cu_seqlens, batch, True)
     _linattn_states(d, dev, h0=h0, dhT=dhT)
 
     def call(handle):

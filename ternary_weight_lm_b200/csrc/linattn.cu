@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   const int col0 = static_cast<int>(blockIdx.z % slices) * kCols;
   if (col0 >= w.dv) return;
   const int h = blockIdx.y;
+  if (!kState && col0 == 0) lin_clear<T>(c, w, h);
   const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
   const bool whole = g.first && g.last;   // an unsplit sequence: nothing to start from
   if (!g.valid || (kState && whole)) return;

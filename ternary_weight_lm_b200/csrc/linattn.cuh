@@ -49,6 +49,7 @@ struct LinCall {
   const float* log_decay;  // [H]
   int64_t seg_len;
   int64_t n_items;
+  int clear;               // zeros for the rows of tokens outside the sequences
   int split;               // segments start from states found by a pass over k and v first
   unsigned* status;
 };

@@ -100,6 +100,22 @@ __device__ __forceinline__ void lin_bounds(const LinCall& c, int b, int64_t* lo,
   if (x != *lo || y != *hi) *bad = true;
 }
 
+// Zeros for the rows of head h of a sweep's output that belong to no sequence, shared out over the
+// blocks of gridDim.x.
+template <typename T>
+__device__ __forceinline__ void lin_clear(const LinCall& c, const LinSweep& w, int h) {
+  if (!c.clear || c.cu == nullptr) return;
+  const int64_t x = __ldg(c.cu), y = __ldg(c.cu + c.B);
+  const int64_t lo = min(max(x, static_cast<int64_t>(0)), c.T), hi = min(max(y, lo), c.T);
+  const int64_t vecs = w.dv * static_cast<int>(sizeof(T)) / 16, n = (lo + c.T - hi) * vecs;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t row = i / vecs, t = row < lo ? row : row - lo + hi;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(w.o) + t * w.o_t + h * w.o_h);
+    o[i - row * vecs] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // A sequence without tokens has one (empty) segment, which passes its state on.
 __device__ __forceinline__ int64_t lin_count(const LinCall& c, int64_t len) {
   return len <= c.seg_len ? 1 : (len + c.seg_len - 1) / c.seg_len;

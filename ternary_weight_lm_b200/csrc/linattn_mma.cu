@@ -128,6 +128,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 
   const LinSweep& w = c.sw[sweep0 + blockIdx.z / tiles];
   const int h = blockIdx.y;
+  if (!kState && blockIdx.z % tiles == 0) lin_clear<__half>(c, w, h);
   const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
   const bool whole = g.first && g.last;        // an unsplit sequence: nothing to start from
   if (!g.valid || (kState && whole)) return;

@@ -266,6 +266,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 
   const int sweep = blockIdx.z, h = blockIdx.y;
   const LinSweep& w = c.sw[sweep];
+  if (!kState) lin_clear<__half>(c, w, h);
   const LinSeg g = lin_find(c, blockIdx.x, w.backwards != 0);
   const bool whole = g.first && g.last;
   if (!g.valid || (kState && whole)) return;

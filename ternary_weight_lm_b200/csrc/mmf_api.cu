@@ -620,6 +620,7 @@ void lin_call(const mmf_linattn_desc* d, int n_sweeps, LinCall* c) {
   c->B = static_cast<int>(d->B);
   c->H = d->H;
   c->cu = d->cu_seqlens;
+  c->clear = d->clear_outside != 0;
   c->log_decay = d->log_decay;
   const int64_t strides[4][2] = {{d->q_t, d->q_h}, {d->k_t, d->k_h}, {d->v_t, d->v_h}, {d->o_t, d->o_h}};
   c->form = lin_form(d->H, d->dk, d->dv, c->dt, n_sweeps, strides);

@@ -42,3 +42,35 @@ def test_long_prompts_of_other_forms(dk, dv, shared):
     plain.assert_close(o.cpu().numpy(), ref, plain.tolerance(ref, mag, True, T, dk), "o")
     plain.assert_close(hT.cpu().numpy(), refT, plain.sum_bound(T, dk) * magT, "hT")
     _check_backward(got, *a, do, h0, dhT, norms=False)
+
+
+# whole and in segments; almost every token outside, and none
+@pytest.mark.parametrize("T,cu", [(300, [3, 40, 170]), (5000, [4000, 4000, 4010]),
+                                  (3000, [0, 2900, 2900]), (300, [7, 7]), (200, [0, 200])])
+@pytest.mark.parametrize("dt,dk,dv", [(np.float16, 128, 128), (np.float16, 64, 64),
+                                      (np.float16, 64, 128), (np.float16, 8, 24),
+                                      (np.float32, 200, 40)])
+def test_rows_outside_the_sequences_are_zero(T, cu, dt, dk, dv):
+    H = 2
+    q, k, v, _ = _make(T, H, dk, dv, dt, seed=T)
+    do = np.roll(v, 1, axis=0)
+    for x in (q, k, v, do):
+        x[:cu[0]] = np.nan
+        x[cu[-1]:] = np.nan
+    dq, dk_, dvv, dd, lg = (to_dev(x) for x in (q, k, v, do, _decays(H)))
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    # memory that the outputs will lie in, full of what must not stay
+    rest = [torch.full((T, H, max(dk, dv)), float("nan"), dtype=dq.dtype, device=DEV)
+            for _ in range(4)]
+    del rest
+    o = mmf.linattn_forward(dq, dk_, dvv, lg, cu_seqlens=cud)
+    grads = mmf.linattn_backward(dq, dk_, dvv, lg, dd, cu_seqlens=cud)[:3]
+    given = torch.full_like(o, 9.0)
+    mmf.linattn_forward(dq, dk_, dvv, lg, cu_seqlens=cud, out=given)
+    torch.cuda.synchronize()
+    assert mmf.mmf_get_device_status() == 0
+    for x in (o, *grads):
+        assert bool((x[:cu[0]] == 0).all()) and bool((x[cu[-1]:] == 0).all())
+    assert bool((given[:cu[0]] == 9).all()) and bool((given[cu[-1]:] == 9).all())
+    assert torch.equal(given[cu[0]:cu[-1]], o[cu[0]:cu[-1]])
+    assert bool(torch.isfinite(o).all())

@@ -57,3 +57,10 @@ def test_segments_are_those_of_the_kernel_that_runs():
     assert len(shared) == 1 and grad(desc(**kw)) not in shared and 0 not in shared
     # heads further apart than a tensor map's columns go
     assert need(desc(**kw, k_h=1 << 30)) == need(desc(**kw, q_h=1 << 62)) == need(desc(**kw, q_t=0))
+
+
+def test_the_descriptor_keeps_its_layout():
+    # clear_outside stands where there was padding
+    d = mmf.LinattnDesc
+    assert (d.scale.offset, d.clear_outside.offset, d.log_decay.offset) == (40, 44, 48)
+    assert ctypes.sizeof(d) == 120
