@@ -508,6 +508,8 @@ def _on(t, stream, call):
             return call(torch._C._cuda_getCurrentRawStream(at))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     with torch.cuda.device(at), torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -566,7 +568,7 @@ def int8_linear_forward(x, W8, wscale, norm_w=None, eps=1e-8, out_dtype=None, ws
 
     def call(handle):
         y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
-        scratch = workspace(mmf_int8_workspace_bytes(T, K), dev) if ws is None else ws
+        scratch = _scratch(ws, max(mmf_int8_workspace_bytes(T, K), 256), dev)
         mmf_int8_forward(x, norm_w, eps, W8, wscale, y, scratch, handle)
         return y
 
@@ -596,8 +598,15 @@ def _linattn(q, k, v, log_decay, o, scale, cu_seqlens, batch, clear=False):
         *k.stride()[:2], *v.stride()[:2], *((H * dv, dv) if o is None else o.stride()[:2]))
 
 
-def _linattn_ws(ws, need, device):
-    return ws if ws is not None or need == 0 else workspace(need, device)
+def _scratch(ws, need, device):
+    """The workspace of a call: the caller's, if it is one, or a new one of `need` bytes."""
+    if ws is None:
+        return workspace(need, device) if need > 0 else None
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws
 
 
 def _linattn_states(d, device, **states):
@@ -625,7 +634,7 @@ def linattn_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, batch=None,
         o = out
         if o is None:
             o = torch.empty((d.T, d.H, d.dv), dtype=q.dtype, device=dev)
-        scratch = _linattn_ws(ws, mmf_linattn_workspace_bytes(d), dev)
+        scratch = _scratch(ws, mmf_linattn_workspace_bytes(d), dev)
         mmf_linattn_forward(d, q, k, v, h0, o, hT, scratch, handle)
         return o
 
@@ -672,7 +681,7 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, batc
         dh0 = None
         if want_dh0:
             dh0 = torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=dev)
-        scratch = _linattn_ws(ws, mmf_linattn_backward_workspace_bytes(d), dev)
+        scratch = _scratch(ws, mmf_linattn_backward_workspace_bytes(d), dev)
         mmf_linattn_backward(d, q, k, v, dout, h0, dhT, dq, dk, dv, dh0, scratch, handle)
         return dq, dk, dv, dh0
 

@@ -64,3 +64,50 @@ def test_the_descriptor_keeps_its_layout():
     d = mmf.LinattnDesc
     assert (d.scale.offset, d.clear_outside.offset, d.log_decay.offset) == (40, 44, 48)
     assert ctypes.sizeof(d) == 120
+
+
+class _OnGpu:
+    """Stands for a tensor on the second GPU."""
+    is_cuda, device = True, torch.device("cuda:1")
+
+    def get_device(self):
+        return 1
+
+
+class _Stream:
+    device, cuda_stream = torch.device("cuda:0"), 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    def call(handle):
+        raise AssertionError("launched")
+
+    with pytest.raises(ValueError, match="stream is on cuda:0"):
+        mmf._on(_OnGpu(), _Stream(), call)
+
+
+def test_a_workspace_elsewhere_is_refused():
+    dev = torch.device("meta")
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        mmf._scratch(torch.zeros(512, dtype=torch.uint8), 512, dev)
+    with pytest.raises(ValueError, match="contiguous"):
+        mmf._scratch(torch.zeros(1024, dtype=torch.uint8, device=dev)[::2], 512, dev)
+    ws = torch.zeros(512, dtype=torch.uint8, device=dev)
+    assert mmf._scratch(ws, 512, dev) is ws and mmf._scratch(None, 0, dev) is None
+    assert mmf._scratch(None, 300, dev).numel() == 300
+
+
+@pytest.mark.parametrize("name", ["linattn_forward", "linattn_backward", "int8_linear_forward"])
+def test_every_call_with_a_workspace_checks_it(name, monkeypatch):
+    # as far as the workspace on the host: the launches are taken away
+    monkeypatch.setattr(mmf, "_on", lambda t, stream, call: call(0))
+    for f in ("mmf_linattn_forward", "mmf_linattn_backward", "mmf_int8_forward"):
+        monkeypatch.setattr(mmf, f, lambda *a: None)
+    x = torch.zeros(4, 2, 16)
+    args = {"linattn_forward": (x, x, x, torch.zeros(2)),
+            "linattn_backward": (x, x, x, torch.zeros(2), x),
+            "int8_linear_forward": (torch.zeros(4, 128), torch.zeros(8, 128, dtype=torch.int8),
+                                    torch.zeros(8))}[name]
+    getattr(mmf, name)(*args, ws=torch.zeros(1 << 16, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="ws is on meta"):
+        getattr(mmf, name)(*args, ws=torch.zeros(1 << 16, dtype=torch.uint8, device="meta"))
