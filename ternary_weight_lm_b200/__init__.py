@@ -494,6 +494,22 @@ def _tensor(name, t, shape, dtypes, device, contiguous=True):
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
+_current = None
+
+
+def _current_calls():
+    """torch's calls for the current device and for a device's current stream as a handle: without
+    their checks (1.3 us a call) where this release has them so, else the public ones."""
+    global _current
+    if _current is None:
+        import torch
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current = (device or torch.cuda.current_device,
+                    handle or (lambda at: torch.cuda.current_stream(at).cuda_stream))
+    return _current
+
+
 def _on(t, stream, call):
     """``call(handle)`` with the tensor's device and the call's stream current, so that what the
     call allocates belongs to the stream that uses it; the handle is the stream's."""
@@ -502,10 +518,11 @@ def _on(t, stream, call):
         raise ValueError(f"tensors must be on a GPU, got {t.device}")
     at = t.get_device()
     if stream is None:
-        if at == torch._C._cuda_getDevice():
-            return call(torch._C._cuda_getCurrentRawStream(at))
+        device, handle = _current or _current_calls()
+        if at == device():
+            return call(handle(at))
         with torch.cuda.device(at):
-            return call(torch._C._cuda_getCurrentRawStream(at))
+            return call(handle(at))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device)
     if stream.device != t.device:

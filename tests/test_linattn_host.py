@@ -111,3 +111,13 @@ def test_every_call_with_a_workspace_checks_it(name, monkeypatch):
     getattr(mmf, name)(*args, ws=torch.zeros(1 << 16, dtype=torch.uint8))
     with pytest.raises(ValueError, match="ws is on meta"):
         getattr(mmf, name)(*args, ws=torch.zeros(1 << 16, dtype=torch.uint8, device="meta"))
+
+
+def test_the_current_stream_without_torchs_private_calls(monkeypatch):
+    for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, n, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda at: type("S", (), {"cuda_stream": 100 + at}))
+    monkeypatch.setattr(mmf, "_current", None)
+    assert mmf._on(_OnGpu(), None, lambda handle: handle) == 101
