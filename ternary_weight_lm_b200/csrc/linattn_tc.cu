@@ -61,6 +61,7 @@ constexpr int kThreads = 640;
 // Registers of the groups' threads; together 5 * 96, what the block is launched with.
 constexpr int kRegsIssue = 40, kRegsState = 184, kRegsDecay = 64, kRegsRows = 96;
 static_assert(kRegsIssue + kRegsState + kRegsDecay + 2 * kRegsRows <= 5 * 96, "registers");
+constexpr int kKeyBits = 6;                  // keys of a chunk that count as alike
 constexpr int kGroup = 128;                  // threads of the state warps, and of the row warps
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -167,11 +168,12 @@ __device__ __forceinline__ int up_to_half(float top) {
 __device__ __forceinline__ float warp_max(float magnitude) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(magnitude)));
 }
-__device__ __forceinline__ float max8(const float (&x)[8]) {
-  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-}
-__device__ __forceinline__ float max4(const float (&x)[4]) {
-  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  return m;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -188,6 +190,14 @@ __device__ __forceinline__ uint32_t row_at(uint32_t tile, int r) {
 }
 __device__ __forceinline__ uint32_t vec_of(uint32_t row, int x) {
   return (row ^ static_cast<uint32_t>((x & 7) << 4)) + static_cast<uint32_t>((x >> 3) * kPanel);
+}
+
+template <int N>
+__device__ __forceinline__ float min_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fminf(m, x[i]);
+  return m;
 }
 
 // Tensor maps of each sweep's k, v and q.
@@ -235,13 +245,17 @@ struct Bars {
   uint64_t q_read, qk, upd, drain;
 };
 
+template <bool kState>
 struct Shared {
   Bars bars;
   float pow[kC + 4];        // gamma^0 .. gamma^128
   LinDecay decay[2];        // of a whole chunk, of the last one
-  float diag[64];           // diag[32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i
-  alignas(16) float col[32];   // gamma^(31-j) forwards, gamma^j backwards
-  float red_k[2][8], red_w[2][8], top_k[2][8], red_s[4];   // of each warp (a panel's four)
+  // diag[skew + 32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i.  In it stand also a
+  // column's powers of the blocks before, gamma^(31-j) forwards, gamma^j backwards, 16-byte aligned
+  alignas(16) float diag[68];
+  float red_k[2][kState ? 8 : 4], red_w[2][kState ? 8 : 4], red_s[4];   // of each warp (a panel's four)
+  float top_k[2][4], low_k[2][4];   // largest magnitudes of rows of K: the largest and the least of each warp
+  uint8_t key[2][kC];               // and each as the exponent of a power of two that it does not pass
   int exp_s[2];             // exponent of the fp16 state, by chunk
   int exp_k[4];             // of K'
   int bad_at[kD];           // first position of the segment whose v is not finite, by column
@@ -249,14 +263,15 @@ struct Shared {
   uint32_t tmem;
   int abort;
 };
-static_assert(Lay<false>::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory per block");
+static_assert(Lay<false>::kSmem + sizeof(Shared<false>) <= 227 * 1024, "shared memory per block");
+static_assert(Lay<true>::kSmem + sizeof(Shared<true>) <= 227 * 1024, "shared memory per block");
 
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps maps) {
   using L = Lay<kState>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared sh;
+  __shared__ Shared<kState> sh;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto tile_k = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage); };
   auto tile_v = [&](int s) { return base + static_cast<uint32_t>(s * L::kStage + kTile); };
@@ -305,16 +320,12 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (!kState) tma_prefetch_desc(mq);
   }
   if (tid <= kC) sh.pow[tid] = lin_power(lin_lg2(c, h), tid);
-  if (tid < 64) {
+  if (!kState && tid < 64) {
     const int d = back ? tid - 32 : 32 - tid;
-    sh.diag[tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
+    sh.diag[(back ? 0 : 3) + tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
   }
   if (tid < 2) sh.decay[tid] = LinDecay(lin_lg2(c, h), tid == 0 || g.n % kC == 0 ? kC : g.n % kC);
-  if (tid < 32) {
-    sh.col[tid] = lin_power(lin_lg2(c, h), back ? tid : 31 - tid);
-  }
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
-  if (tid < 16) sh.red_k[tid >> 3][tid & 7] = sh.red_w[tid >> 3][tid & 7] = sh.top_k[tid >> 3][tid & 7] = 0.0f;
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), L::kCols);
     tmem_relinquish();
@@ -422,16 +433,21 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       }
     }
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
-    const float most = warp_max(top);
+    if constexpr (!kState) sh.key[set][r] = static_cast<uint8_t>((__float_as_uint(top) + 0x7fffffu) >> 23);
+    const float most = kState ? 0.0f : warp_max(top);
+    const float least = kState ? 0.0f : __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(in ? top : 65504.0f)));
     top = warp_max(top * fabsf(wt));
     if (lane == 0) {
       const int at = (r >> 5) + 4 * panel;
       sh.red_k[set][at] = top;
       sh.red_w[set][at] = wide;
-      sh.top_k[set][at] = most;
+      if constexpr (!kState) {
+        sh.top_k[set][at] = most;
+        sh.low_k[set][at] = least;
+      }
     }
     if (!named_bar_and(id, kState ? 2 * kGroup : kGroup, ok)) return false;
-    const int e = min(up_to_half(max8(sh.red_k[set])), up_to_half(max8(sh.red_w[set])));
+    const int e = min(up_to_half(max_of(sh.red_k[set])), up_to_half(max_of(sh.red_w[set])));
     if (r == 0 && panel == 0) sh.exp_k[chunk & 3] = e;
     *f = wt * pow2(e);
     return true;
@@ -590,10 +606,10 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     }
     // the state for chunk ch: scaled, rounded and written as the B operand of Q S
     auto publish = [&](int ch, bool ok) {
-      const float m = warp_max(max4(top));
+      const float m = warp_max(max_of(top));
       if (lane == 0) sh.red_s[q] = m;
       if (!named_bar_and(1, kGroup, ok)) return false;
-      const int e = up_to_half(max4(sh.red_s));
+      const int e = up_to_half(max_of(sh.red_s));
       if (r == 0) sh.exp_s[ch & 1] = e;
       const uint64_t f2 = pair(pow2(e), pow2(e));
       const uint32_t s_row = row_at(tile_s, r);
@@ -711,13 +727,32 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       };
       for (int ch = turn; ch < chunks; ch += 2) {
         const int ph = (ch >> 1) & 1;
-        // The row's power of two, from a bound on its scores, 128 max|q_i| max|k|: a few bits more
-        // than they have, of the 29 between fp16's largest and smallest normal values.
+        // The row's power of two, from a bound on its scores, 128 max|q_i| max|k|: a few bits more than
+        // they have, of the 29 between fp16's largest and smallest normal values.  Where the chunk's
+        // keys differ by more than 2^kKeyBits, a later one, or one that has decayed away, would cost too
+        // many: there over the tokens up to the row's own and decayed, max gamma^(i-j) |k_j| (for all chunks
+        // it takes 3 % longer).
         if (!wait(sh.bars.q_full[turn], ph)) break;
         const float top_q = row_top(row_at(tile_q, r));
         arrive(sh.bars.q_read);
         if (!wait(sh.bars.v[turn], ph)) break;
-        const int e = up_to_half(top_q * max8(sh.top_k[turn]) * (128.0f * fabsf(w.a)));
+        float most = max_of(sh.top_k[turn]);
+        if (min_of(sh.low_k[turn]) * static_cast<float>(1 << kKeyBits) < most) {
+          auto key = [&](int row) { return __uint_as_float(static_cast<uint32_t>(sh.key[turn][row]) << 23); };
+          // up to each row's token: of the warp's rows (scanned; a lane without a neighbour that far gets
+          // the outermost one's, which does no harm), then of the blocks before them
+          most = key(r);
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1)
+            most = fmaxf(most, __shfl_sync(0xffffffffu, most, max(0, min(31, back ? lane + o : lane - o))) * sh.pow[o]);
+          float before = 0.0f;
+#pragma unroll 1
+          for (int b = b0; b <= b1; ++b)
+            if (b != q)
+              before = fmaxf(before, key(32 * b + lane) * sh.pow[back ? 32 * (b - q) + lane - 31 : 32 * (q - b) - lane]);
+          most = fmaxf(most, warp_max(before) * sh.pow[back ? 31 - lane : lane]);
+        }
+        const int e = up_to_half(top_q * most * (128.0f * fabsf(w.a)));
         const bool bad = *reinterpret_cast<volatile int*>(&sh.any_bad) != 0;
         const bool bad_k = bad || tokens(ch) < kC;   // rows past the end may hold anything
         if (!wait(sh.bars.scores[turn], ph)) break;
@@ -735,7 +770,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
               const uint64_t f2 = pair(f, f);
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(&sh.col[j]);
+                const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(&sh.diag[(back ? 32 : 4) + j]);
                 const float2 x = unpair(mul2(pair(__uint_as_float(d[j]), __uint_as_float(d[j + 1])),
                                              mul2(c4.x, f2)));
                 const float2 y = unpair(mul2(pair(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])),
@@ -750,7 +785,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
                 for (int j = 0; j < 32; ++j)
                   if (back ? j < lane : j > lane) d[j] = 0u;
               }
-              const float* pw = sh.diag + 32 - lane;
+              const float* pw = sh.diag + (back ? 32 : 35) - lane;
 #pragma unroll
               for (int j = 0; j < 32; j += 2)
                 u[j / 2] = pack2(__uint_as_float(d[j]) * (pw[j] * f), __uint_as_float(d[j + 1]) * (pw[j + 1] * f));

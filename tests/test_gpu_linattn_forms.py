@@ -74,3 +74,55 @@ def test_rows_outside_the_sequences_are_zero(T, cu, dt, dk, dv):
     assert bool((given[:cu[0]] == 9).all()) and bool((given[cu[-1]:] == 9).all())
     assert torch.equal(given[cu[0]:cu[-1]], o[cu[0]:cu[-1]])
     assert bool(torch.isfinite(o).all())
+
+
+def _floor(q, k, v, decay, scale):
+    """What fp16's smallest step can add to an output of the chunked forms, for one sequence.
+
+    A score's power of two brings its row's largest, or a bound on it, to 2^14 .. 2^15.  The bound is
+    at most 2^6 times 128 max|q_i| max_j gamma^(i-j) |k_j| (max|k| of keys within 2^6 of one another;
+    else the decayed maximum, of keys rounded up to powers of two); half a step of 2^-24 among the
+    subnormals is then at most 2^-25 / 2^14 2^6 = 2^-33 of that, times |v_j|.  A state likewise
+    brings its largest value, at most the decayed sum of max|k_j| max|v_j|, there: at most 2^-39
+    of it, times |q_i|."""
+    q, k, v = (np.abs(x.astype(np.float64)) for x in (q, k, v))
+    g = plain.gammas(decay)
+    reach, state = np.zeros(len(g)), np.zeros(len(g))
+    out, vs = np.empty(v.shape), np.zeros(v.shape[1:])
+    for t in range(len(q)):
+        reach = np.maximum(reach * g, k[t].max(axis=-1))
+        state = state * g + k[t].max(axis=-1) * v[t].max(axis=-1)
+        vs = vs + v[t]
+        out[t] = ((2.0 ** -33 * 128 * q[t].max(axis=-1) * reach)[:, None] * vs +
+                  (2.0 ** -39 * q[t].sum(axis=-1) * state)[:, None])
+    return scale * out
+
+
+# A key far larger than the rest, of a later token or of one that has decayed away, must not cost the
+# others their bits: all values within their own bounds.  Backwards the keys are dout (for dk) and q
+# (for dv), and later tokens come first.
+@pytest.mark.parametrize("d", [128, 64, 40])
+@pytest.mark.parametrize("lg", [0.0, -0.7])
+def test_a_large_key_does_not_cost_others_their_bits(d, lg):
+    T, H, at, scale = 200, 2, 100, 2.0 ** -8    # the largest results stay below fp16's 65504
+    q, k, v, _ = _make(T, H, d, d, np.float16, seed=60)
+    do = np.roll(v, 5, axis=0)
+    small = np.float16(1e-4)
+    decay = np.full(H, lg, dtype=np.float32)
+    kk, qq, dd = k * small, q * small, do * small
+    for x in (kk, qq, dd):
+        x[at, :, 7] = 60000.0
+    o = mmf.linattn_forward(to_dev(q), to_dev(kk), to_dev(v), to_dev(decay), scale=scale)
+    ref, _ = plain.linattn(q, kk, v, decay, [0, T], scale)
+    mag, _ = plain.absolute(plain.linattn, q, kk, v, decay, [0, T], scale)
+    plain.assert_close(o.cpu().numpy(), ref, plain.tolerance(ref, mag, True, T, d) +
+                       _floor(q, kk, v, decay, scale), "o")
+    for q, k, v, do in ((q, k, v, dd), (qq, k, v, do)):
+        got = mmf.linattn_backward(*(to_dev(x) for x in (q, k, v, decay, do)), scale=scale)
+        a = (q, k, v, decay, [0, T], scale, do)
+        mags = plain.absolute(plain.linattn_backward, *a)
+        floors = (_floor(do, v, k, decay, scale),
+                  _floor(v[::-1], do[::-1], q[::-1], decay, scale)[::-1],
+                  _floor(k[::-1], q[::-1], do[::-1], decay, scale)[::-1])
+        for name, x, ref, mag, low in zip(("dq", "dk", "dv"), got, plain.linattn_backward(*a), mags, floors):
+            plain.assert_close(x.cpu().numpy(), ref, plain.tolerance(ref, mag, True, T, d) + low, name)
