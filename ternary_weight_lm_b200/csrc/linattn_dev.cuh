@@ -49,6 +49,10 @@ __device__ __forceinline__ float lin_power(double lg2, int64_t n) {
   return n == 0 ? 1.0f : exp2f(static_cast<float>(lg2 * static_cast<double>(n)));
 }
 
+// A factor kept finite in fp16.  Only a token whose values are all zero can have a larger one (the scales
+// come from the others), and its products have to stay zero.
+__device__ __forceinline__ float lin_half_range(float w) { return fminf(fmaxf(w, -65504.0f), 65504.0f); }
+
 // The decay gamma^n of a state that is carried on many times, as whole + part, whole 1 or 0.  Rounded to
 // one float it would be off the same way every time (a log decay of -1e-4: 9e-5 of a state after 4096
 // tokens).  part is off by 2^-24 of 1 - gamma^n (of gamma^n below a half, where a state lasts for a few

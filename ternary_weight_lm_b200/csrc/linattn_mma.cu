@@ -452,7 +452,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const int j = 16 * kk + 2 * t4 + 8 * z;
-        const float w0 = weight(j) * fv, w1 = weight(j + 1) * fv;
+        const float w0 = lin_half_range(weight(j) * fv), w1 = lin_half_range(weight(j + 1) * fv);
         const __half2 wh = __floats2half2_rn(w0, w1);
         const float2 r = __half22float2(wh);
         const __half2 wl = __floats2half2_rn(w0 - r.x, w1 - r.y);

@@ -449,7 +449,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (!named_bar_and(id, kState ? 2 * kGroup : kGroup, ok)) return false;
     const int e = min(up_to_half(max_of(sh.red_k[set])), up_to_half(max_of(sh.red_w[set])));
     if (r == 0 && panel == 0) sh.exp_k[chunk & 3] = e;
-    *f = wt * pow2(e);
+    *f = lin_half_range(wt * pow2(e));
     return true;
   };
   auto decay_k = [&](int chunk, int r, int panel, float f) {

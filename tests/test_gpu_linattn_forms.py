@@ -76,18 +76,19 @@ def test_rows_outside_the_sequences_are_zero(T, cu, dt, dk, dv):
     assert bool(torch.isfinite(o).all())
 
 
-def _floor(q, k, v, decay, scale):
+def _floor(q, k, v, decay, scale, h0=None):
     """What fp16's smallest step can add to an output of the chunked forms, for one sequence.
 
     A score's power of two brings its row's largest, or a bound on it, to 2^14 .. 2^15.  The bound is
     at most 2^6 times 128 max|q_i| max_j gamma^(i-j) |k_j| (max|k| of keys within 2^6 of one another;
     else the decayed maximum, of keys rounded up to powers of two); half a step of 2^-24 among the
     subnormals is then at most 2^-25 / 2^14 2^6 = 2^-33 of that, times |v_j|.  A state likewise
-    brings its largest value, at most the decayed sum of max|k_j| max|v_j|, there: at most 2^-39
-    of it, times |q_i|."""
+    brings its largest value, at most the decayed sum of max|k_j| max|v_j| and the start's, there: at
+    most 2^-39 of it, times |q_i|."""
     q, k, v = (np.abs(x.astype(np.float64)) for x in (q, k, v))
     g = plain.gammas(decay)
-    reach, state = np.zeros(len(g)), np.zeros(len(g))
+    reach = np.zeros(len(g))
+    state = reach if h0 is None else np.abs(h0[0].astype(np.float64)).max(axis=(1, 2))
     out, vs = np.empty(v.shape), np.zeros(v.shape[1:])
     for t in range(len(q)):
         reach = np.maximum(reach * g, k[t].max(axis=-1))
@@ -96,6 +97,14 @@ def _floor(q, k, v, decay, scale):
         out[t] = ((2.0 ** -33 * 128 * q[t].max(axis=-1) * reach)[:, None] * vs +
                   (2.0 ** -39 * q[t].sum(axis=-1) * state)[:, None])
     return scale * out
+
+
+def _backward_floors(q, k, v, decay, scale, do, h0=None):
+    """Of dq, dk and dv, each a sweep of its own."""
+    flip = None if h0 is None else np.swapaxes(h0, 2, 3)
+    return (_floor(do, v, k, decay, scale, flip),
+            _floor(v[::-1], do[::-1], q[::-1], decay, scale)[::-1],
+            _floor(k[::-1], q[::-1], do[::-1], decay, scale)[::-1])
 
 
 # A key far larger than the rest, of a later token or of one that has decayed away, must not cost the
@@ -121,8 +130,39 @@ def test_a_large_key_does_not_cost_others_their_bits(d, lg):
         got = mmf.linattn_backward(*(to_dev(x) for x in (q, k, v, decay, do)), scale=scale)
         a = (q, k, v, decay, [0, T], scale, do)
         mags = plain.absolute(plain.linattn_backward, *a)
-        floors = (_floor(do, v, k, decay, scale),
-                  _floor(v[::-1], do[::-1], q[::-1], decay, scale)[::-1],
-                  _floor(k[::-1], q[::-1], do[::-1], decay, scale)[::-1])
+        floors = _backward_floors(q, k, v, decay, scale, do)
         for name, x, ref, mag, low in zip(("dq", "dk", "dv"), got, plain.linattn_backward(*a), mags, floors):
             plain.assert_close(x.cpu().numpy(), ref, plain.tolerance(ref, mag, True, T, d) + low, name)
+
+
+# Rows of zeros where the rest of a chunk has decayed away, as padding with zeros has them; and
+# gradients far below 1 of a length that no chunk divides.  (Where only v is zero, the scores of those
+# tokens are what the others' step is set by: _floor.)
+@pytest.mark.parametrize("d", [128, 64, 40])
+@pytest.mark.parametrize("lg", [-0.1, -0.7, -3.0])
+@pytest.mark.parametrize("zero", ["k", "v", "kv", "qkv", ""])
+def test_rows_of_zeros_and_small_gradients(d, lg, zero):
+    T, H, scale = 210, 2, 0.1
+    q, k, v, h0 = _make(T, H, d, d, np.float16, seed=70, h0=True)
+    do = np.roll(v, 5, axis=0) * np.float16(1e-3)
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        if name in zero:
+            x[30:64] = 0
+            x[90:200] = 0
+    decay = np.full(H, lg, dtype=np.float32)
+    a = (q, k, v, decay, [0, T], scale)
+    hT = torch.empty(1, H, d, d, device=DEV)
+    o = mmf.linattn_forward(*(to_dev(x) for x in a[:4]), scale=scale, h0=to_dev(h0), hT=hT)
+    ref, refT = plain.linattn(*a, h0)
+    mag, magT = plain.absolute(plain.linattn, *a, h0=h0)
+    plain.assert_close(o.cpu().numpy(), ref, plain.tolerance(ref, mag, True, T, d) +
+                       _floor(q, k, v, decay, scale, h0), "o")
+    plain.assert_close(hT.cpu().numpy(), refT, plain.sum_bound(T, d) * magT, "hT")
+    for grad in (do, np.where(np.arange(T)[:, None, None] % 70 < 30, do, do * 0)):
+        got = mmf.linattn_backward(*(to_dev(x) for x in (*a[:4], grad)), scale=scale,
+                                   h0=to_dev(h0), want_dh0=True)
+        refs = plain.linattn_backward(*a, grad, h0)
+        mags = plain.absolute(plain.linattn_backward, *a, grad, h0=h0)
+        floors = _backward_floors(q, k, v, decay, scale, grad, h0)
+        for name, x, r, m, low in zip(("dq", "dk", "dv", "dh0"), got, refs, mags, (*floors, 0.0)):
+            plain.assert_close(x.cpu().numpy(), r, plain.tolerance(r, m, name != "dh0", T, d) + low, name)
