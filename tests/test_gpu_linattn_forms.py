@@ -166,3 +166,57 @@ def test_rows_of_zeros_and_small_gradients(d, lg, zero):
         floors = _backward_floors(q, k, v, decay, scale, grad, h0)
         for name, x, r, m, low in zip(("dq", "dk", "dv", "dh0"), got, refs, mags, (*floors, 0.0)):
             plain.assert_close(x.cpu().numpy(), r, plain.tolerance(r, m, name != "dh0", T, d) + low, name)
+
+
+# bounds that descend, overlap or leave the tokens, for every kernel, whole and in segments (heads of
+# 128 take their rows by tensor map): nothing outside the outputs is touched, and it is reported
+@pytest.mark.parametrize("cu", [[0, 500, 200, 600], [-50, 100, 700, 9000], [600, 0, 600, 0],
+                                [2147483647, -2147483648, 5, 9], [0, 4000, 0, 4000, 0, 4000]])
+@pytest.mark.parametrize("T", [600, 4000])
+@pytest.mark.parametrize("dt,d", [(np.float16, 128), (np.float16, 64), (np.float16, 24),
+                                  (np.float32, 128)])
+def test_bad_bounds_forwards_and_backwards(cu, T, dt, d):
+    H, B, pad = 2, len(cu) - 1, 300
+    q, k, v, h0 = _make(T, H, d, d, dt, seed=2, B=B, h0=True)
+    dq, dk, dv, lg = (to_dev(x) for x in (q, k, v, _decays(H)))
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    if T == 4000:
+        assert _need(dq, dk, dv, lg, cu=cud) > 0
+        assert _need(dq, dk, dv, lg, cu=cud, dout=dv) > 0
+    rows = [torch.full((T + 2 * pad, H, d), 7.0, dtype=dq.dtype, device=DEV) for _ in range(4)]
+    o, gq, gk, gv = (x[pad:-pad] for x in rows)
+    states = [torch.full((B + 2, H, d, d), 7.0, device=DEV) for _ in range(3)]
+    s0, sT, ds = (x[1:-1] for x in states)
+    s0.copy_(to_dev(h0))
+    mmf.linattn_forward(dq, dk, dv, lg, cu_seqlens=cud, h0=s0, hT=sT, out=o)
+    torch.cuda.synchronize()
+    assert mmf.mmf_get_device_status() == 8
+    # into buffers with guards, which the convenience does not take
+    d_ = mmf._linattn(dq, dk, dv, lg, dv, None, cud, None)
+    need = mmf.mmf_linattn_backward_workspace_bytes(d_)
+    ws = mmf.workspace(need) if need else None
+    mmf.mmf_linattn_backward(d_, dq, dk, dv, dv, s0, sT, gq, gk, gv, ds, ws)
+    torch.cuda.synchronize()
+    assert mmf.mmf_get_device_status() == 8
+    for x in rows:
+        assert bool((x[:pad] == 7).all()) and bool((x[-pad:] == 7).all())
+    for x in states:
+        assert bool((x[0] == 7).all()) and bool((x[-1] == 7).all())
+    assert torch.equal(s0, to_dev(h0))
+
+
+# Which calls are cut into segments: few heads of a long prompt, not many of them nor a short one
+@pytest.mark.parametrize("T,H,d,split", [
+    (2700, 40, 128, True), (1300, 300, 128, False), (300, 4, 128, False),
+    (2700, 40, 64, True), (4000, 8, 64, True), (1300, 444, 64, False), (100, 4, 64, False)])
+def test_which_calls_are_split(T, H, d, split):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    q, k, v = (torch.randn(T, H, d, generator=g, device=DEV).half() for _ in range(3))
+    lg, heads = to_dev(_decays(H)), [0, 1, H - 1]
+    assert (_need(q, k, v, lg) > 0) == split
+    o = mmf.linattn_forward(q, k, v, lg)
+    a = [x[:, heads].cpu().numpy() for x in (q, k, v)]
+    ref, _ = plain.linattn(*a, _decays(H)[heads], [0, T], d ** -0.5)
+    mag, _ = plain.absolute(plain.linattn, *a, _decays(H)[heads], [0, T], d ** -0.5)
+    got = o[:, heads].cpu().numpy()
+    plain.assert_close(got, ref, plain.tolerance(ref, mag, True, T, d), "o")
