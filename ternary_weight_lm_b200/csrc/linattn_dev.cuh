@@ -2,6 +2,8 @@
 // that a block works on.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "linattn.cuh"
 #include "ptx.cuh"
 
@@ -49,9 +51,13 @@ __device__ __forceinline__ float lin_power(double lg2, int64_t n) {
   return n == 0 ? 1.0f : exp2f(static_cast<float>(lg2 * static_cast<double>(n)));
 }
 
-// A factor kept finite in fp16.  Only a token whose values are all zero can have a larger one (the scales
-// come from the others), and its products have to stay zero.
-__device__ __forceinline__ float lin_half_range(float w) { return fminf(fmaxf(w, -65504.0f), 65504.0f); }
+// Factors in fp16, kept finite.  Only a token whose values are all zero can have one beyond its range (the
+// scales come from the others), and its products have to stay zero.
+__device__ __forceinline__ __half2 lin_half2_finite(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return *reinterpret_cast<const __half2*>(&v);
+}
 
 // The decay gamma^n of a state that is carried on many times, as whole + part, whole 1 or 0.  Rounded to
 // one float it would be off the same way every time (a log decay of -1e-4: 9e-5 of a state after 4096
@@ -60,7 +66,6 @@ __device__ __forceinline__ float lin_half_range(float w) { return fminf(fmaxf(w,
 // part x alone rounded into x, decays next to 1 would come to nothing.
 struct LinDecay {
   float whole, part;
-  LinDecay() = default;
   __device__ __forceinline__ LinDecay(double lg2, int64_t n) {
     const double g = n == 0 ? 1.0 : exp2(lg2 * static_cast<double>(n));
     whole = g >= 0.5 ? 1.0f : 0.0f;
@@ -69,6 +74,26 @@ struct LinDecay {
   // gamma^n x + u
   __device__ __forceinline__ float next(float x, float u) const {
     return fmaf(whole, x, fmaf(part, x, u));
+  }
+};
+
+// The decay gamma^n of chunks of n tokens, for states that take a chunk's product in the same operation,
+// gamma^n x + u rounded once, where u moves the rounding about.  Rounded to one float the decay would be
+// off the same way every time (4.7e-6 of a state after 16384 tokens at a log decay of -1e-4), so the two
+// floats around it take turns, in proportion.  `last`: of the `left` tokens of a shorter last chunk.
+struct LinTurns {
+  float lo, hi, share, last;
+  LinTurns() = default;
+  __device__ __forceinline__ LinTurns(double lg2, int n, int left) {
+    const double g = exp2(lg2 * n);
+    lo = __double2float_rd(g);
+    hi = __double2float_ru(g);
+    share = hi > lo ? static_cast<float>((g - lo) / (static_cast<double>(hi) - lo)) : 0.0f;
+    last = left == 0 ? 1.0f : static_cast<float>(exp2(lg2 * left));
+  }
+  __device__ __forceinline__ float of(int chunk) const {
+    const float x = static_cast<float>(chunk);
+    return floorf(fmaf(x, share, share + 0.5f)) > floorf(fmaf(x, share, 0.5f)) ? hi : lo;
   }
 };
 

@@ -124,7 +124,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float s_pow[kC + 1];     // gamma^0 .. gamma^64
   __shared__ int s_exp[kC];           // exponent of each row of P
-  __shared__ LinDecay s_decay[2];     // of a whole chunk, of the last one
+  __shared__ LinTurns s_decay;
 
   const LinSweep& w = c.sw[sweep0 + blockIdx.z / tiles];
   const int h = blockIdx.y;
@@ -138,7 +138,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   const int lag = w.backwards ? 1 : 0;
   const double lg2 = lin_lg2(c, h);
   if (tid <= kC) s_pow[tid] = lin_power(lg2, tid);
-  if (tid < 2) s_decay[tid] = LinDecay(lg2, tid == 0 || g.n % kC == 0 ? kC : g.n % kC);
+  if (tid == 0) s_decay = LinTurns(lg2, kC, static_cast<int>(g.n % kC));
 
   const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
@@ -232,6 +232,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
     cp_async_wait<kStages - 2>();
     __syncthreads();                  // the chunk is in, and the one before it is done with
     load(chunk + kStages - 1);
+    const float decay = n < kC ? s_decay.last : s_decay.of(static_cast<int>(chunk));
     bool strange = false;             // the warp's part of V has a value that is not finite
 
     if constexpr (!kState) {
@@ -452,10 +453,10 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const int j = 16 * kk + 2 * t4 + 8 * z;
-        const float w0 = lin_half_range(weight(j) * fv), w1 = lin_half_range(weight(j + 1) * fv);
-        const __half2 wh = __floats2half2_rn(w0, w1);
+        const float w0 = weight(j) * fv, w1 = weight(j + 1) * fv;
+        const __half2 wh = lin_half2_finite(w0, w1);
         const float2 r = __half22float2(wh);
-        const __half2 wl = __floats2half2_rn(w0 - r.x, w1 - r.y);
+        const __half2 wl = lin_half2_finite(w0 - r.x, w1 - r.y);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -467,7 +468,6 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
             lo[kk][m][2 * z + y] = *reinterpret_cast<const uint32_t*>(&l2);
           }
       }
-    const LinDecay decay = s_decay[n < kC];
     const float back = pow2(-ev);
     top = 0.0f;
     constexpr int NG = 4;             // column tiles of S^T at a time
@@ -504,7 +504,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float& y = S[m][n0 + x][e];
-            y = decay.next(y, D[m][x][e] * back);
+            y = fmaf(decay, y, D[m][x][e] * back);
             if constexpr (!kState) {
               if (e & 1) top = max3_abs(top, S[m][n0 + x][e - 1], y);
             }

@@ -249,7 +249,7 @@ template <bool kState>
 struct Shared {
   Bars bars;
   float pow[kC + 4];        // gamma^0 .. gamma^128
-  LinDecay decay[2];        // of a whole chunk, of the last one
+  LinTurns decay;
   // diag[skew + 32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i.  In it stand also a
   // column's powers of the blocks before, gamma^(31-j) forwards, gamma^j backwards, 16-byte aligned
   alignas(16) float diag[68];
@@ -324,7 +324,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int d = back ? tid - 32 : 32 - tid;
     sh.diag[(back ? 0 : 3) + tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
   }
-  if (tid < 2) sh.decay[tid] = LinDecay(lin_lg2(c, h), tid == 0 || g.n % kC == 0 ? kC : g.n % kC);
+  if (tid == 0) sh.decay = LinTurns(lin_lg2(c, h), kC, static_cast<int>(g.n % kC));
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), L::kCols);
@@ -449,15 +449,16 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     if (!named_bar_and(id, kState ? 2 * kGroup : kGroup, ok)) return false;
     const int e = min(up_to_half(max_of(sh.red_k[set])), up_to_half(max_of(sh.red_w[set])));
     if (r == 0 && panel == 0) sh.exp_k[chunk & 3] = e;
-    *f = lin_half_range(wt * pow2(e));
+    *f = wt * pow2(e);
     return true;
   };
   auto decay_k = [&](int chunk, int r, int panel, float f) {
     const uint32_t row = row_at(tile_k(chunk & 1) + panel * kPanel, r);
     const uint32_t row2 = row_at(tile_lo(chunk & 1) + panel * kPanel, r);
     const bool in = (back ? kC - 1 - r : r) < tokens(chunk);
-    const __half fh = __float2half_rn(f);
-    const __half2 wh = __half2half2(fh), wl = __float2half2_rn(f - __half2float(fh));
+    const __half2 wh = lin_half2_finite(f, f);
+    const float rest = f - __low2float(wh);
+    const __half2 wl = lin_half2_finite(rest, rest);
 #pragma unroll
     for (int x0 = 0; x0 < kVecs; x0 += 8) {
       uint4 v[8];
@@ -633,10 +634,9 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
       const bool w2 = wait(sh.bars.upd, ch & 1);
       if (w2) {
         tc_fence_after();
-        const LinDecay decay = sh.decay[tokens(ch) < kC];
+        const float decay = tokens(ch) < kC ? sh.decay.last : sh.decay.of(ch);
         const float f = pow2(-sh.exp_k[ch & 3]);
-        const uint64_t whole2 = pair(decay.whole, decay.whole), part2 = pair(decay.part, decay.part);
-        const uint64_t f2 = pair(f, f);
+        const uint64_t decay2 = pair(decay, decay), f2 = pair(f, f);
         top[0] = top[1] = top[2] = top[3] = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -646,7 +646,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             uint64_t& x = S[16 * b + i];
-            x = fma2(whole2, x, fma2(part2, x, mul2(pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), f2)));
+            x = fma2(decay2, x, mul2(pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), f2));
             if constexpr (!kState) {
               const float2 y = unpair(x);
               top[i & 3] = max3_abs(top[i & 3], y.x, y.y);
