@@ -280,8 +280,9 @@ mmf_status mmf_bitlinear_backward(const void* x, mmf_dtype xdt, int64_t T, int64
  *   s_n  = max_k |W_nk| / 127
  *   c_nk = clamp(round_half_even(W_nk / s_n), -127, 127)   (divisions in float; s_n = 0: code 0)
  *   y_tn = (sum_k q_tk c_nk) * (gamma_t / 127 * s_n)       (sum exact in int32, then float)
- * Shapes: 1 <= T <= 16777216; N % 8 == 0, 8 <= N <= 2^20; K % 16 == 0, 16 <= K <= 32768 (for
- * mmf_int8_forward, whose pre-pass takes the forward's K: K % 128 == 0, K <= 8192).  All matrices
+ * Shapes: 1 <= T <= 16777216; N % 8 == 0, 8 <= N <= 2^20; K % 16 == 0, 16 <= K <= 32768.  The
+ * library makes activation codes for K % 128 == 0, K <= 8192 alone (mmf_quantize_activations, and
+ * with it mmf_int8_forward); for other K the codes and gamma come from the caller.  All matrices
  * row-major and contiguous, 16-byte aligned, W finite.  Errors as for the forward.  Asynchronous
  * on `stream`. */
 mmf_status mmf_int8_quantize_weights(const void* W, mmf_dtype wdt, int64_t N, int64_t K,
@@ -310,14 +311,24 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  *   S_t = gamma_h S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   gamma_h = exp(log_decay_h)
  * log_decay: [H] floats on the device, at most 0; values above 0 and NaN count as 0 (no decay),
  * -inf is a decay of 0 (a token sees itself alone).  States are fp32 [B x H x dk x dv], sums and
- * states are held in fp32.
+ * states are held in fp32, and a decay's own rounding does not add up over tokens or calls.
+ * Of dtype fp32, and of fp16 with dk other than 64 and 128 or dv no multiple of 64 (gradients: dv
+ * other than 64 and 128), all products are fp32 too.  The other fp16 sizes go to the tensor cores,
+ * and operands made on the way are rounded for them, each scaled by a power of two first:
+ *   the scores q.k, decayed, to 11 bits, and no finer than 2^-33 of 128 max|q_t| max|k| over the
+ *     keys up to its own token, decayed;
+ *   the state that a chunk of tokens starts from, as an operand of S^T q, to 11 bits, and no finer
+ *     than 2^-39 of its largest value (of 128 x 128: of the whole state, else of 16 or 32 columns);
+ *   the decayed k or v of the state's update, to 22 bits, and no finer than 2^-39 of the largest
+ *     in its chunk (of the largest factor, where k or v is below 1).
+ * So an output has about 2^-11 of the sum of its terms' magnitudes beside its own rounding.  |scale|
+ * is taken without loss from 2^-40 to 2^40.
  *
  * q, k [T x H x dk], v, o [T x H x dv], all of dtype dt, the last dimension contiguous; *_t and
  * *_h are the strides of a token and of a head in elements, multiples of 16 bytes, not negative
  * (0 shares a row between heads or tokens; not for o, whose rows have no value in common, nor for
- * dout).  Tokens are packed: with cu_seqlens
- * ([B + 1] int32 on the device, ascending, within 0..T) sequence b has the tokens
- * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
+ * dout).  Tokens are packed: with cu_seqlens ([B + 1] int32 on the device, ascending, within 0..T)
+ * sequence b has the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
  * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are not read, and not
  * written either unless clear_outside asks for zeros in their rows of o, dq, dk and dv.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is
  * touched, the outputs are then unspecified and mmf_get_device_status returns MMF_ERR_PLAN.
@@ -325,7 +336,8 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  * 256.  Pointers to matrices are 16-byte aligned, ws is 256-byte aligned (NULL with ws_bytes 0
  * when the query gives 0).  The workspace holds nothing between calls; calls that may overlap
  * need one each.  Outputs overlap no input (but hT may be h0).  A value that is not finite reaches
- * no earlier token and no other sequence; what depends on it is not finite.  Errors as for the
+ * no earlier token and no other sequence; what depends on it is not finite (an infinity in a state
+ * becomes NaN).  Errors as for the
  * forward.  Asynchronous on `stream`; may be captured into a CUDA graph. */
 typedef struct {
   int64_t T;                    /* tokens of all sequences */
@@ -366,7 +378,8 @@ mmf_status mmf_linattn_backward(const mmf_linattn_desc* d, const void* q, const 
  * NULL with n_slots 0: row b has state b.  Otherwise state has n_slots states and slots[b]
  * (device) names row b's; a negative slot is padding: o is zeros and no state is touched.  The
  * same goes for a slot from n_slots on and for one that an earlier row has named already;
- * mmf_get_device_status then returns MMF_ERR_PLAN. */
+ * mmf_get_device_status then returns MMF_ERR_PLAN.  (To find those, each head of row b reads the b
+ * slots before it.) */
 mmf_status mmf_linattn_step(const mmf_linattn_desc* d, const void* q, const void* k,
                             const void* v, void* o, float* state, const int32_t* slots,
                             int64_t n_slots, void* stream);

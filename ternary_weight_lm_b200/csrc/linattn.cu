@@ -442,9 +442,12 @@ void lin_plan(int64_t T, int64_t B, bool ragged, int H, int dk, int dv, LinForm 
   // A model of the time, of the kernel that the call takes.  A block handles `step` tokens at a
   // time and `each` of them run on an SM (blocks beyond 148 each wait for the next wave); a step
   // takes t0 + t1 n us with n blocks on an SM, a block's start and end `start` us, a pass over k and v
-  // alone about half of a whole one, and the two launches that a split adds `more` us.  Times measured on 16 heads of 128 or 64 and, in fp32, 8
-  // of 128: a step of 128 tokens with tcgen05 4.1; of 64 in the register form 3.4 alone on an SM, 7
-  // with three; of 16 token by token 3.2 alone, 6.1 with three.  The split is worth (us, split /
+  // alone about half of a whole one, and the two launches that a split adds `more` us.  The constants were
+  // fitted to whole calls (16 heads of 128 or 64, in fp32 8 of 128), so they hold a part of the starts and
+  // of the last, shorter segments.  A step alone, measured from the slope over long sequences: 128 tokens with
+  // tcgen05 4.4; 64 in the register form 2.9 alone on an SM, 5.0 with three; 16 token by token 4.9
+  // with three.  With these for constants the model would choose other segments in one call of ten, and
+  // by itself gain 1 % at most on the average.  The split is worth (us, split /
   // whole): one prompt of 1024 28 / 36, of 4096 45 / 125, heads of 64, 4 of 512 21 / 30, fp32, one of
   // 512 40 / 104; it is not: backward of 1024 40 / 36, heads of 64, 8 of 512 35 / 31.
   const bool tc = form == kLinTc, mma = form == kLinMma;

@@ -45,8 +45,10 @@ __device__ __forceinline__ double lin_lg2_of(float log_decay) {
 __device__ __forceinline__ double lin_lg2(const LinCall& c, int h) {
   return lin_lg2_of(__ldg(c.log_decay + h));
 }
-// gamma^n: the exponent is multiplied in double and rounded once to float (an error of at most
-// n |log2 gamma| 2^-24 relative to the power); gamma^0 is 1 for every decay.
+// gamma^n: the exponent is multiplied in double and rounded once to float, which puts at most
+// n |log2 gamma| 2^-24 on the power, relative to it; exp2f's own error, up to 2 ulp, comes on top and is
+// the larger one while n |log2 gamma| is small.  For weights that are used once; a state's decay is
+// LinDecay or LinTurns.  gamma^0 is 1 for every decay.
 __device__ __forceinline__ float lin_power(double lg2, int64_t n) {
   return n == 0 ? 1.0f : exp2f(static_cast<float>(lg2 * static_cast<double>(n)));
 }

@@ -22,7 +22,9 @@
 // stay in the instruction cache.
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
-// K' scaled by powers of two (a row's, the state's, the chunk's) before they are rounded.  The
+// K' scaled by powers of two (a row's, the whole state's, the chunk's) before they are rounded, and what is
+// more than 2^28 (K': 2^18) below the largest under its power loses bits to fp16's subnormals; P's power
+// comes from a bound, some 2^10 above the scores, so 2^18 there too.  The
 // state takes a chunk's product in one fp32 rounding.
 //
 // A v that is not finite would reach earlier tokens through P V as 0 times infinity.  Such values
@@ -35,9 +37,9 @@
 // What bounds it.  Bytes that the sweep cannot do without: 128 KB a chunk (3 us of an SM's share of
 // the HBM).  Five products of 512 cycles on the tensor pipe, which read both operands from shared
 // memory at all of its bandwidth, and about 1800 cycles more of that for the conversions: no unit is
-// full, the hand-overs between them and the fetch of the roles' code fill the rest.  Measured: 5.0 us
-// a chunk; 32768 tokens of 16 heads in 147 us, their states alone (kState, 64 KB a chunk) in 67; whole
-// call 240 us (a register form on mma.sync: 553, two of its waves; token by token: 2991).
+// full, the hand-overs between them and the fetch of the roles' code fill the rest.  Measured: 4.4 us
+// a chunk, 5.0 where every row comes from HBM; 32768 tokens of 16 heads in 150 us, their states alone
+// (kState, 64 KB a chunk) in 68; whole call 240 us (a register form on mma.sync: 553, two of its waves; token by token: 2991).
 //
 // Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
 // copies and MMAs in flight are drained and TMEM is freed.
