@@ -83,19 +83,21 @@ struct LinDecay {
 // gamma^n x + u rounded once, where u moves the rounding about.  Rounded to one float the decay would be
 // off the same way every time (4.7e-6 of a state after 16384 tokens at a log decay of -1e-4), so the two
 // floats around it take turns, in proportion.  `last`: of the `left` tokens of a shorter last chunk.
-struct LinTurns {
-  float lo, hi, share, last;
+struct alignas(16) LinTurns {
+  float lo, hi;
+  uint32_t share;   // of the turns that are hi's, in 2^-32
+  float last;
   LinTurns() = default;
   __device__ __forceinline__ LinTurns(double lg2, int n, int left) {
     const double g = exp2(lg2 * n);
     lo = __double2float_rd(g);
     hi = __double2float_ru(g);
-    share = hi > lo ? static_cast<float>((g - lo) / (static_cast<double>(hi) - lo)) : 0.0f;
+    share = hi > lo ? __double2uint_rn((g - lo) / (static_cast<double>(hi) - lo) * 0x1p32) : 0u;
     last = left == 0 ? 1.0f : static_cast<float>(exp2(lg2 * left));
   }
   __device__ __forceinline__ float of(int chunk) const {
-    const float x = static_cast<float>(chunk);
-    return floorf(fmaf(x, share, share + 0.5f)) > floorf(fmaf(x, share, 0.5f)) ? hi : lo;
+    // hi when a sum of shares, from a half on, passes a whole one
+    return (static_cast<uint32_t>(chunk) + 1u) * share + 0x80000000u < share ? hi : lo;
   }
 };
 

@@ -27,7 +27,7 @@ namespace {
 constexpr int64_t kMaxT = 16777216;
 constexpr int64_t kMaxK = 8192;
 constexpr int64_t kMaxN = 1 << 20;
-constexpr int64_t kMaxK8 = 32768;   // 8-bit projection: 128 * 127 * 32768 < 2^31
+constexpr int64_t kMaxK8 = 32768;   // 8-bit projection: sums to 128 * 128 * 32768 = 2^29
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
