@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   __shared__ __align__(16) float s_v[kTok][2 * kCols];
   __shared__ float s_o[kState ? 1 : 4][kState ? 1 : kTok][kCols];
   __shared__ float s_up[kTok + 1], s_down[kTok + 1];   // gamma^-n, gamma^n; 1 for fast decays
+  __shared__ LinDecay s_decay[2];
 
   const int slices = (max(c.sw[0].dv, c.sw[0].dk) + kCols - 1) / kCols;
   const LinSweep& w = c.sw[blockIdx.z / slices];
@@ -90,11 +91,12 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   const double lg2 = lin_lg2(c, h);
   const int lag = w.backwards ? 1 : 0;   // backwards the decay acts after a token, not before it
   const bool slow = lg2 * kTok >= -8.0;
-  const LinDecay decay(lg2, slow ? kTok : 1);
-  if (tid <= kTok) {
-    s_up[tid] = slow ? static_cast<float>(exp2(-lg2 * tid)) : 1.0f;
-    s_down[tid] = slow ? static_cast<float>(exp2(lg2 * tid)) : 1.0f;
-  }
+  // the decay still due after the last token: of the last tile's tokens, of one backwards, or none
+  const int64_t left = g.n == 0 ? 0 : slow ? (g.n - 1) % kTok + 1 : lag;
+  if (tid <= kTok) s_up[tid] = slow ? static_cast<float>(exp2(-lg2 * tid)) : 1.0f;
+  if (tid >= 32 && tid <= 32 + kTok) s_down[tid - 32] = slow ? static_cast<float>(exp2(lg2 * (tid - 32))) : 1.0f;
+  if (tid == 64) s_decay[0] = LinDecay(lg2, slow ? kTok : 1);
+  if (tid == 96) s_decay[1] = LinDecay(lg2, left);
   const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
 
@@ -139,11 +141,12 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
     rv = (p0 + tok < g.n && d < w.dv) ? ld4<T>(vp + g.token(p0 + tok) * w.v_t + d) : zero4;
   };
 
-  // the decay that the state has still to take, with the next token of the full form
-  LinDecay due = decay;
-  if (slow || lag) due.whole = 1.0f, due.part = 0.0f;
   fetch(0);
   __syncthreads();
+  // the decay that the state has still to take, with the next token of the full form
+  const LinDecay decay = s_decay[0];
+  LinDecay due = decay;
+  if (slow || lag) due.whole = 1.0f, due.part = 0.0f;
   const float va = w.a * s_up[tid / (kCols / 4) + 1 - lag];
   for (int64_t p0 = 0; p0 < g.n; p0 += kTok) {
 #pragma unroll
@@ -222,9 +225,7 @@ __global__ void __launch_bounds__(kSweepThreads, KR == 16 ? 2 : 3) lin_sweep_ker
   }
 
   if (!kState && !(whole && w.sT)) return;
-  // the decay still due: of the last tile's tokens, of the last token backwards, or none
-  const int64_t left = g.n == 0 ? 0 : slow ? (g.n - 1) % kTok + 1 : lag;
-  const LinDecay end(lg2, left);
+  const LinDecay end = s_decay[1];
 #pragma unroll
   for (int i = 0; i < KR; ++i)
 #pragma unroll
@@ -251,9 +252,14 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
   const int e = (static_cast<int>(blockIdx.x) % blocks * 256 + static_cast<int>(threadIdx.x)) * 4;
   int64_t first, len;
   const int64_t n = lin_segments(c, b, &first, &len);   // whole warps
-  if (n < 2 || e >= w.dk * w.dv) return;
-  const double lg2 = lin_lg2(c, h);
-  const LinDecay gl(lg2, c.seg_len), glast(lg2, max(len - (n - 1) * c.seg_len, static_cast<int64_t>(0)));
+  if (n < 2) return;   // all threads
+  __shared__ LinDecay s_decay[2];
+  if (threadIdx.x < 2)
+    s_decay[threadIdx.x] = LinDecay(lin_lg2(c, h), threadIdx.x == 0 ? c.seg_len
+                                    : max(len - (n - 1) * c.seg_len, static_cast<int64_t>(0)));
+  __syncthreads();
+  if (e >= w.dk * w.dv) return;
+  const LinDecay gl = s_decay[0], glast = s_decay[1];
   const int i = e / w.dv, j = e % w.dv;
   const size_t state = static_cast<size_t>(w.dk) * w.dv;
   const size_t at = (static_cast<size_t>(b) * c.H + h) * state + static_cast<size_t>(i) * w.s_key +
@@ -344,13 +350,15 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_con
     s_k[tid] = ld1<T>(kp + tid);
     s_q[tid] = ld1<T>(qp + tid);
   }
-  const LinDecay gamma(lin_lg2_of(c.log_decay[h]), 1);
+  __shared__ LinDecay s_decay;
+  if (tid == kStepThreads - 1) s_decay = LinDecay(lin_lg2_of(c.log_decay[h]), 1);
   const int col = col0 + 4 * lane;
   const bool in = col < c.dv;
   const float4 v4 = in ? ld4<T>(vp + col) : make_float4(0.f, 0.f, 0.f, 0.f);
   float* st = c.state + (static_cast<size_t>(slot) * c.H + h) * c.dk * c.dv + col;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
+  const LinDecay gamma = s_decay;
   for (int r0 = warp; in && r0 < c.dk; r0 += kStepWarps * kUnroll) {
     float4 x[kUnroll];
 #pragma unroll

@@ -68,6 +68,7 @@ __device__ __forceinline__ __half2 lin_half2_finite(float lo, float hi) {
 // part x alone rounded into x, decays next to 1 would come to nothing.
 struct LinDecay {
   float whole, part;
+  LinDecay() = default;
   __device__ __forceinline__ LinDecay(double lg2, int64_t n) {
     const double g = n == 0 ? 1.0 : exp2(lg2 * static_cast<double>(n));
     whole = g >= 0.5 ? 1.0f : 0.0f;

@@ -139,7 +139,6 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
   const int lag = w.backwards ? 1 : 0;
   const double lg2 = lin_lg2(c, h);
   if (tid <= kC) s_pow[tid] = lin_power(lg2, tid);
-  if (tid == 0) s_decay = LinTurns(lg2, kC, static_cast<int>(g.n % kC));
 
   const size_t state0 = (static_cast<size_t>(g.seq) * c.H + h) * w.dk * w.dv;
   float* seg = w.seg ? w.seg + (static_cast<size_t>(blockIdx.x) * c.H + h) * w.dk * w.dv : nullptr;
@@ -227,6 +226,7 @@ lin_mma_kernel(const __grid_constant__ LinCall c, int sweep0, int tiles) {
 
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(i);
+  if (tid == 0) s_decay = LinTurns(lg2, kC, static_cast<int>(g.n % kC));
   for (int64_t chunk = 0; chunk < chunks; ++chunk) {
     const int s = static_cast<int>(chunk % kStages);
     const int n = static_cast<int>(min(static_cast<int64_t>(kC), g.n - chunk * kC));

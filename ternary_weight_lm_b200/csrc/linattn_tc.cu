@@ -326,7 +326,7 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const int d = back ? tid - 32 : 32 - tid;
     sh.diag[(back ? 0 : 3) + tid] = d >= 0 ? lin_power(lin_lg2(c, h), d) : 0.0f;
   }
-  if (tid == 0) sh.decay = LinTurns(lin_lg2(c, h), kC, static_cast<int>(g.n % kC));
+  if (tid == kThreads - 1) sh.decay = LinTurns(lin_lg2(c, h), kC, static_cast<int>(g.n % kC));
   if (tid < kD) sh.bad_at[tid] = 0x7fffffff;
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh.tmem), L::kCols);
