@@ -313,8 +313,9 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  * -inf is a decay of 0 (a token sees itself alone).  States are fp32 [B x H x dk x dv], sums and
  * states are held in fp32, and a decay's own rounding does not add up over tokens or calls.
  * Of dtype fp32, and of fp16 with dk other than 64 and 128 or dv no multiple of 64 (gradients: dv
- * other than 64 and 128), all products are fp32 too.  The other fp16 sizes go to the tensor cores,
- * and operands made on the way are rounded for them, each scaled by a power of two first:
+ * other than 64 and 128), all products are fp32 too (sums have room to 2^119).  The other fp16
+ * sizes go to the tensor cores, and operands made on the way are rounded for them, each scaled by a
+ * power of two first:
  *   the scores q.k, decayed, to 11 bits, and no finer than 2^-33 of 128 max|q_t| max|k| over the
  *     keys up to its own token, decayed;
  *   the state that a chunk of tokens starts from, as an operand of S^T q, to 11 bits, and no finer
@@ -328,17 +329,18 @@ mmf_status mmf_int8_forward(const void* x, mmf_dtype xdt, int64_t T, int64_t K,
  * *_h are the strides of a token and of a head in elements, multiples of 16 bytes, not negative
  * (0 shares a row between heads or tokens; not for o, whose rows have no value in common, nor for
  * dout).  Tokens are packed: with cu_seqlens ([B + 1] int32 on the device, ascending, within 0..T)
- * sequence b has the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B sequences of T / B tokens
- * (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are not read, and not
- * written either unless clear_outside asks for zeros in their rows of o, dq, dk and dv.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is
- * touched, the outputs are then unspecified and mmf_get_device_status returns MMF_ERR_PLAN.
+ * sequence b has the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and may have none; NULL means B
+ * sequences of T / B tokens (T % B == 0).  Tokens before cu_seqlens[0] and from cu_seqlens[B] on are
+ * not used, and not written either unless clear_outside asks for zeros in their rows of o, dq, dk
+ * and dv.  Bounds that descend or leave 0..T are clamped, so nothing outside the tensors is touched,
+ * the outputs are then unspecified and mmf_get_device_status returns MMF_ERR_PLAN.
  * Shapes: 1 <= T <= 16777216, 1 <= B <= 2^20, 1 <= H <= 4096, dk and dv multiples of 8 from 8 to
  * 256.  Pointers to matrices are 16-byte aligned, ws is 256-byte aligned (NULL with ws_bytes 0
  * when the query gives 0).  The workspace holds nothing between calls; calls that may overlap
  * need one each.  Outputs overlap no input (but hT may be h0).  A value that is not finite reaches
  * no earlier token and no other sequence; what depends on it is not finite (an infinity in a state
- * becomes NaN).  Errors as for the
- * forward.  Asynchronous on `stream`; may be captured into a CUDA graph. */
+ * becomes NaN).  Errors as for the forward.  Asynchronous on `stream`; may be captured into a CUDA
+ * graph. */
 typedef struct {
   int64_t T;                    /* tokens of all sequences */
   int64_t B;                    /* sequences */

@@ -17,18 +17,18 @@
 // power of two that brings its largest value to 2^14 .. 2^15: P (a power for each row, from its largest
 // score), the state in Q S (one for each warp's columns and chunk), and the decayed V of the state's
 // update (likewise).  So fp16's range does not matter, and its subnormals do for what is more than 2^28
-// below the largest under the same power (in two parts, as the update's: more than 2^18).  P and the state cost a rounding of 2^-11 each, of different parts of an output
-// that is rounded to 2^-11 itself.  The decayed V is carried as two fp16 parts, 22 bits: the state
-// is an fp32 output, and a third rounding would cost more than it saves (one part alone, measured:
-// error against 64 bits 0.00035 instead of 0.00029, the output's own rounding being 0.00021).  All
-// sums are fp32; the state takes a chunk's product in one fp32 rounding, so the tensor cores' own
-// accumulation spans 64 tokens.
+// below the largest under the same power (in two parts, as the update's: more than 2^18).  P and the
+// state cost a rounding of 2^-11 each, of different parts of an output that is rounded to 2^-11 itself.
+// The decayed V is carried as two fp16 parts, 22 bits: the state is an fp32 output, and a third rounding
+// would cost more than it saves (one part alone, measured: error against 64 bits 0.00035 instead of
+// 0.00029, the output's own rounding being 0.00021).  All sums are fp32; the state takes a chunk's
+// product in one fp32 rounding, so the tensor cores' own accumulation spans 64 tokens.
 //
 // What bounds it.  Heads of 64: 64 tokens are 32 KB, 0.7 us of an SM's share of the HBM; the products
 // 0.5 us of mma.sync (555 TFLOP/s measured on this part).  Neither is reached: at 12 warps an SM the
 // issue and latency of about 1800 instructions a warp and chunk are what counts (0.4 of a scheduler's
 // slots).  Measured: 13 ragged prompts of 9001 tokens, 16 heads of 64, 41 us, their states 23, a call
-// 73 us (with the registers for a fourth block on an SM, spilling, a tenth more; for two: as three,
+// 71 us (with the registers for a fourth block on an SM, spilling, a tenth more; for two: as three,
 // backward a fifth slower).  Four warps with a quarter of the columns each, because a warp with 32
 // columns uses every operand it loads from Q, K and P twice: with 16 the loads would take as long as
 // the products.

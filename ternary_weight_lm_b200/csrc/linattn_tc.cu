@@ -18,14 +18,15 @@
 // outputs overlap the other's scores.  Registers go from the first group to the state's.
 // K' has two fp16 parts (22 bits), so that the state, an fp32 output, keeps its precision; the first
 // overwrites K once Q K^T is done.  Shared memory, 32 KB each: two stages of K and V, the second
-// part of K', Q (loaded again as soon as Q S is done), the fp16 state.  TMEM: P, Q S, P V, V^T K', 128 columns each; the fp16 P overwrites P.  Loops over blocks of columns are not unrolled: the groups' code together has to
-// stay in the instruction cache.
+// part of K', Q (loaded again as soon as Q S is done), the fp16 state.  TMEM: P, Q S, P V, V^T K', 128
+// columns each; the fp16 P overwrites P.  Loops over blocks of columns are not unrolled: the groups' code
+// together has to stay in the instruction cache.
 //
 // Numbers: as in the register form of this sweep (linattn_mma.cu): Q, K, V exact; P, the state and
-// K' scaled by powers of two (a row's, the whole state's, the chunk's) before they are rounded, and what is
-// more than 2^28 (K': 2^18) below the largest under its power loses bits to fp16's subnormals; P's power
-// comes from a bound, some 2^10 above the scores, so 2^18 there too.  The
-// state takes a chunk's product in one fp32 rounding.
+// K' scaled by powers of two (a row's, the whole state's, the chunk's) before they are rounded, and what
+// is more than 2^28 (K': 2^18) below the largest under its power loses bits to fp16's subnormals.  P's
+// power comes from a bound, some 2^10 above the scores, so 2^18 there too.  The state takes a chunk's
+// product in one fp32 rounding.
 //
 // A v that is not finite would reach earlier tokens through P V as 0 times infinity.  Such values
 // are replaced by zero on arrival and their place is noted: from that token on the column's
@@ -39,7 +40,8 @@
 // memory at all of its bandwidth, and about 1800 cycles more of that for the conversions: no unit is
 // full, the hand-overs between them and the fetch of the roles' code fill the rest.  Measured: 4.4 us
 // a chunk, 5.0 where every row comes from HBM; 32768 tokens of 16 heads in 150 us, their states alone
-// (kState, 64 KB a chunk) in 68; whole call 240 us (a register form on mma.sync: 553, two of its waves; token by token: 2991).
+// (kState, 64 KB a chunk) in 68; whole call 240 us (a register form on mma.sync: 553, two of its waves;
+// token by token: 2991).
 //
 // Every wait is bounded; on a timeout the block records kStatusTimeout, every role stops, the
 // copies and MMAs in flight are drained and TMEM is freed.
@@ -252,7 +254,7 @@ struct Shared {
   Bars bars;
   float pow[kC + 4];        // gamma^0 .. gamma^128
   LinTurns decay;
-  // diag[skew + 32 - row + column]: gamma^(i-j) of a diagonal block, 0 if j > i.  In it stand also a
+  // diag[32 - row + column], from 3 on forwards: gamma^(i-j) of a diagonal block, 0 if j > i.  In it stand also a
   // column's powers of the blocks before, gamma^(31-j) forwards, gamma^j backwards, 16-byte aligned
   alignas(16) float diag[68];
   float red_k[2][kState ? 8 : 4], red_w[2][kState ? 8 : 4], red_s[4];   // of each warp (a panel's four)
@@ -437,7 +439,8 @@ lin_tc_kernel(const __grid_constant__ LinCall c, const __grid_constant__ LinMaps
     const float wide = warp_max(top != 0.0f ? fabsf(wt) : 0.0f);
     if constexpr (!kState) sh.key[set][r] = static_cast<uint8_t>((__float_as_uint(top) + 0x7fffffu) >> 23);
     const float most = kState ? 0.0f : warp_max(top);
-    const float least = kState ? 0.0f : __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(in ? top : 65504.0f)));
+    const float least =
+        kState ? 0.0f : __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(in ? top : 65504.0f)));
     top = warp_max(top * fabsf(wt));
     if (lane == 0) {
       const int at = (r >> 5) + 4 * panel;
